@@ -255,6 +255,91 @@ mla_status mla_attend_order_a(const mla_dims *dims, const void *qa, const void *
                               const mla_cache *cache, const int32_t *seq_lens, int32_t B, int32_t n_q, void *o,
                               void *ws, size_t ws_bytes, void *stream);
 
+/* Block tables and slot map of one step, from the requests' lengths (no
+ * counterpart on the pages: how cached rows get their pages). Request b holds
+ * ctx_lens[b] cached tokens, whose ceil(ctx / block_size) pages are in row b of
+ * the table, and brings new_lens[b] >= 0 new ones (NULL: one each). In request
+ * order, its missing pages come from the front of free_blocks:
+ *   block_table[b][ceil(ctx / bs) + k] = free_blocks[first_b + k],
+ *     k < ceil((ctx + new) / bs) - ceil(ctx / bs), first_b the blocks before b;
+ *   seq_lens[b] = ctx + new                        (what mla_decode reads);
+ *   row_start[b] = sum of new_lens before b, row_start[B] = their total;
+ *   row t = row_start[b] + i, i < new_lens[b]: seq_idx[t] = b, positions[t] =
+ *     ctx + i (what mla_cache_append reads), slots[t] = the cache row of
+ *     (b, ctx + i) (what mla_cache_write reads); rows row_start[B] <= t < T are
+ *     padding: seq_idx -1, position 0, slot -1;
+ *   used[0] = blocks taken from free_blocks.
+ * shared_blocks (num_shared >= 0 full pages of a prefix common to the batch)
+ * are written to the first num_shared table entries of every request, whose
+ * ctx_lens must count their tokens. All other table entries are left as they
+ * are. Inputs are not changed, so that a step planned twice gives the same.
+ * A request that cannot be planned (a negative length, a context shorter than
+ * the shared pages, more tokens than a table row holds, free_blocks or the T
+ * rows running out) raises MLA_ERR_DEVICE_DATA: its seq_lens entry is 0, its
+ * rows are padding and its table row is left as it is; the others are planned.
+ * (Later requests that need a block, or a row, then run out too.) A page
+ * number outside the pool raises MLA_ERR_DEVICE_DATA; rows on it get slot -1.
+ *   cache: paged; its geometry is read (block_size, max_blocks_per_seq,
+ *     num_blocks, num_seqs >= B), its data and block_table are not touched
+ *   block_table [B][cache->max_blocks_per_seq], updated in place
+ *   ctx_lens, new_lens, seq_lens [B], row_start [B + 1], seq_idx, positions [T],
+ *   used [1]: int32 device; slots [T]: int64 device. B <= 16384. */
+mla_status mla_batch_plan(const mla_cache *cache, int32_t *block_table, const int32_t *ctx_lens,
+                          const int32_t *new_lens, int32_t B, const int32_t *free_blocks, int32_t num_free,
+                          const int32_t *shared_blocks, int32_t num_shared, int32_t T, int32_t *seq_lens,
+                          int32_t *row_start, int32_t *seq_idx, int32_t *positions, int64_t *slots, int32_t *used,
+                          void *stream);
+
+/* Ready latent rows [c_KV | k_R] (computed elsewhere: a prefill worker, a host
+ * copy, another page) stored by a slot map: cache row slots[t] = rows[t].
+ *   rows [T][D]   slots [T] int64 device, distinct where not negative
+ * A negative slot is padding (mla_batch_plan's) and is skipped; a slot past
+ * the cache raises MLA_ERR_DEVICE_DATA and is skipped. Other cache rows keep
+ * their contents. */
+mla_status mla_cache_write(const mla_dims *dims, const void *rows, const int64_t *slots, int32_t T,
+                           const mla_cache *cache, void *stream);
+
+/* Expansion of a prefix (MLA walk-through, section 3 order A): the first
+ * prefix_len positions of cached sequence seq, decompressed once into
+ *   kc[h][i] = W_UK_h c_KV_i,  v[h][i] = W_UV_h c_KV_i  [n_h][prefix_len][d_h],
+ *   kr[i] = k_R,i  [prefix_len][d_r],
+ * storage dtype, rounded once. The caller keeps the three tensors for as long
+ * as requests start with that prefix (2 n_h d_h + d_r numbers per token: 64 KB
+ * at DeepSeek-V2 dims) and passes them to mla_decode_shared. No workspace. A
+ * position whose page is out of range raises MLA_ERR_DEVICE_DATA and expands
+ * to zeros. The tensor-core path needs block_size to be a multiple of 64. */
+mla_status mla_prefix_expand(const mla_dims *dims, const mla_cache *cache, int32_t seq, int32_t prefix_len,
+                             const void *W_UK, const void *W_UV, void *kc, void *v, void *kr, void *stream);
+
+/* Decode of a batch whose sequences share their first prefix_len positions:
+ * order A over the expanded prefix, read once for the whole batch, and order B
+ * over each sequence's own positions, as one softmax. For token row t = b*n_q + j,
+ * head h, with the positions and causal rule of mla_decode (seq_lens[b] counts
+ * the prefix and the new tokens):
+ *   s_i = scale (q_C . kc[h][i] + q_R . kr[i]),  v_i = v[h][i],       i < prefix_len,
+ *   s_i = scale (W_UK_h^T q_C . c_KV_i + q_R . k_R,i),  v_i = W_UV_h c_KV_i,
+ *                                       prefix_len <= i <= L_b - n_q + j,
+ *   o[t][h] = sum_i softmax_i(s) v_i,  lse[t][h] = log sum_i exp(s_i):
+ * the o of mla_decode followed by mla_out_proj, up to rounding.
+ *   qa [B*n_q][n_h][d_h + d_r] (mla_query_heads)   W_UK, W_UV [n_h*d_h][d_c]
+ *   kc, v, kr: from mla_prefix_expand (may be NULL when prefix_len is 0)
+ *   o (output) [B*n_q][n_h*d_h]   lse (output, may be NULL) [B*n_q][n_h] float32
+ * The cache is read at positions prefix_len .. only; with a paged cache the
+ * table entries of the prefix are not read. The tensor-core path needs
+ * block_size, and with a paged cache prefix_len, to be multiples of 64; it
+ * rounds W_UK_h^T q_C, the suffix's latent readout and that readout after W_UV
+ * once each to the storage dtype, as mla_absorb_q, mla_decode and mla_out_proj
+ * do. seq_lens[b] < prefix_len + n_q or beyond the cache capacity raises
+ * MLA_ERR_DEVICE_DATA and leaves that sequence's outputs unwritten.
+ * When it pays: against mla_decode over tables that share the prefix's pages, a
+ * prefix token costs 82 instead of 279 Kflop per row, and 64 KB per batch
+ * instead of 1.1 KB per row (from L2, mostly); below about 32 rows mla_decode
+ * is the faster call. */
+mla_status mla_decode_shared(const mla_dims *dims, const void *qa, const void *kc, const void *v, const void *kr,
+                             int32_t prefix_len, const mla_cache *cache, const int32_t *seq_lens, int32_t B,
+                             int32_t n_q, const void *W_UK, const void *W_UV, void *o, float *lse, void *ws,
+                             size_t ws_bytes, void *stream);
+
 /* Self-test of the failure path (no counterpart on the pages). Launches one
  * small projection kernel whose copy engine is told to issue nothing, so that
  * its MMA thread's bounded wait runs out after wait_ns nanoseconds; the kernel
@@ -271,11 +356,12 @@ mla_status mla_selftest_timeout(uint64_t wait_ns, void *scratch, size_t scratch_
  * every row); mla_decode itself requires the size for max_seq_len = the
  * cache's capacity (max_len, or max_blocks_per_seq * block_size). For
  * MLA_OP_ATTEND_A, max_seq_len is the number of physical cache rows
- * (num_blocks * block_size, or num_seqs * max_len). */
+ * (num_blocks * block_size, or num_seqs * max_len). For MLA_OP_DECODE_SHARED,
+ * rows is B and max_seq_len the prefix length. */
 enum {
   MLA_OP_APPEND = 0, MLA_OP_ABSORB = 1, MLA_OP_DECODE = 2, MLA_OP_OUT_PROJ = 3, MLA_OP_O_PROJ = 4,
   MLA_OP_O_PROJ_LATENT = 5, MLA_OP_ABSORB_MERGED = 6, MLA_OP_FRONT_END = 7, MLA_OP_ABSORB_WO = 8,
-  MLA_OP_QUERY_HEADS = 9, MLA_OP_ATTEND_A = 10
+  MLA_OP_QUERY_HEADS = 9, MLA_OP_ATTEND_A = 10, MLA_OP_PREFIX_EXPAND = 11, MLA_OP_DECODE_SHARED = 12
 };
 size_t mla_workspace_size(const mla_dims *dims, int32_t op, int32_t rows, int32_t n_q,
                           int64_t max_seq_len, int32_t num_splits);

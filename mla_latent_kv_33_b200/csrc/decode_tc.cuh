@@ -141,6 +141,7 @@ struct Params {
   // [BJ + 1], then (splits > 0) piece offsets [BJ + 1]
   int32_t *plan;
   int32_t splits;   // 0: automatic plan; S > 0: every row in min(S, tiles) pieces
+  int32_t skip;     // kSkip instances: leading positions of every sequence left out (a multiple of 64 when paged)
 };
 
 // Offsets of the plan arrays in Params::plan.
@@ -149,8 +150,11 @@ __host__ __device__ constexpr int plan_pieces(int BJ) { return 6 + BJ; }
 
 // The tile line's units are the token rows in query-position-major order:
 // unit u = j B + b is row b n_q + j (new token j of sequence b). The kernel
-// is compiled twice: kGrouped = false serves n_q = 1, where unit and row
-// coincide, with none of the index arithmetic or cluster groups below.
+// is compiled twice for n_q: kGrouped = false serves n_q = 1, where unit and
+// row coincide, with none of the index arithmetic or cluster groups below.
+// kSkip instances attend to positions p.skip .. of every sequence only (the
+// rest of a shared prefix's batch); tiles and lengths below then count from
+// p.skip.
 template <bool kGrouped>
 __device__ __forceinline__ int row_of_unit(const Params &p, int u) {
   return !kGrouped ? u : (u % p.B) * p.n_q + u / p.B;
@@ -160,14 +164,15 @@ __device__ __forceinline__ int unit_of_row(const Params &p, int bj) {
 }
 
 // Tiles visible to unit u; -1 if its sequence length is invalid.
-template <bool kGrouped>
+template <bool kGrouped, bool kSkip>
 __device__ __forceinline__ int unit_tiles(const Params &p, int u, int *vis_out) {
   const int b = !kGrouped ? u : u % p.B, j = !kGrouped ? 0 : u / p.B;
-  const int L = p.seq_lens[b];
-  if (L < p.n_q || static_cast<int64_t>(L) > p.capacity) {
+  int L = p.seq_lens[b];
+  if (L < (kSkip ? p.n_q + p.skip : p.n_q) || static_cast<int64_t>(L) > p.capacity) {
     *vis_out = 0;
     return -1;
   }
+  if (kSkip) L -= p.skip;
   const int vis = L - p.n_q + 1 + j;
   *vis_out = vis;
   return (vis + TILE - 1) / TILE;
@@ -180,15 +185,19 @@ __device__ __forceinline__ int unit_tiles(const Params &p, int u, int *vis_out) 
 // checks and converts their values. The producers issue the loads of tile
 // i + 2 while they convert those of tile i + 1, loaded a whole tile earlier,
 // so that the check (a branch on the loaded value) never waits for memory.
+template <bool kSkip>
 __device__ __forceinline__ void tile_blocks(const Params &p, int b, int64_t t0, int vis, int32_t blk[4]) {
+  if (kSkip) t0 += p.skip, vis += p.skip;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int64_t pos = t0 + BLK * v;
     blk[v] = p.paged && pos < vis ? p.block_table[static_cast<int64_t>(b) * p.max_blocks_per_seq + pos / p.block_size] : 0;
   }
 }
+template <bool kSkip>
 __device__ __forceinline__ void rows_of_blocks(const Params &p, int b, int64_t t0, int vis, const int32_t blk[4],
                                                int32_t r4[4]) {
+  if (kSkip) t0 += p.skip, vis += p.skip;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int64_t pos = t0 + BLK * v;
@@ -228,13 +237,13 @@ __device__ __forceinline__ int split_piece_of(int r, int nt, int sp, int *end) {
 // row that continues into another cluster); base is the first tile of the
 // cluster's group. Forced splits: pieces are also cut at the row's piece
 // boundaries, and the slot is the piece's global index.
-template <bool kGrouped>
+template <bool kGrouped, bool kSkip>
 struct PieceIter {
   int g, gend, u, off, poff, Qt, k, S, base;
   __device__ bool next(const Params &p, Piece &pc) {
     while (g < gend) {
       int vis;
-      int nt = unit_tiles<kGrouped>(p, u, &vis);
+      int nt = unit_tiles<kGrouped, kSkip>(p, u, &vis);
       if (nt < 0) nt = 0;
       if (nt == 0 || off + nt <= g) {
         off += nt;
@@ -345,7 +354,7 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar_local, uint32_t rank)
     mbar_arrive_cluster(mapa_shared(bar_local, 0));
 }
 
-template <bool kGrouped>
+template <bool kGrouped, bool kSkip>
 __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     k_decode(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v0,
@@ -404,7 +413,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
   int *pieces = tiles + BJ;
   for (int u = threadIdx.x; u < BJ; u += NUM_THREADS) {
     int vis;
-    int nt = unit_tiles<kGrouped>(p, u, &vis);
+    int nt = unit_tiles<kGrouped, kSkip>(p, u, &vis);
     if (nt < 0) {
       if (blockIdx.x == 0 && u < p.B) dev_error(MLA_DEVERR_DATA);  // once per sequence
       nt = 0;
@@ -478,7 +487,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
   cluster_sync_all();  // peer barriers initialised, TMEM allocated in both CTAs
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  PieceIter<kGrouped> it0;
+  PieceIter<kGrouped, kSkip> it0;
   it0.g = plan_s[0];
   it0.gend = plan_s[1];
   it0.Qt = max(1, plan_s[2]);
@@ -498,7 +507,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     // arms its full barrier, then lane l issues box l of the item.
     const int w = warp < WARP_MMA ? warp : 3;  // producer index
     const uint32_t q_full = rank == 0 ? bar(BAR_Q_FULL) : mapa_shared(bar(BAR_Q_FULL), 0);
-    PieceIter<kGrouped> it = it0;
+    PieceIter<kGrouped, kSkip> it = it0;
     Piece pc;
     int nbig = 0, nsmall = 0, npc = 0;
     bool ok = true;
@@ -561,9 +570,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     };
     while (ok && it.next(p, pc)) {
       const int b = pc.bj / p.n_q;
-      auto blocks_of = [&](int ti, int32_t *blk) { tile_blocks(p, b, static_cast<int64_t>(ti) * TILE, pc.vis, blk); };
+      auto blocks_of = [&](int ti, int32_t *blk) { tile_blocks<kSkip>(p, b, static_cast<int64_t>(ti) * TILE, pc.vis, blk); };
       auto rows_of = [&](int ti, const int32_t *blk, int32_t *r4) {
-        rows_of_blocks(p, b, static_cast<int64_t>(ti) * TILE, pc.vis, blk, r4);
+        rows_of_blocks<kSkip>(p, b, static_cast<int64_t>(ti) * TILE, pc.vis, blk, r4);
       };
       int32_t cur[4], prev[4], nxt[4] = {0, 0, 0, 0}, raw0[4], raw[4] = {0, 0, 0, 0};
       blocks_of(pc.t_begin, raw0);
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == WARP_MMA) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0 && lane == 0) {
-      PieceIter<kGrouped> it = it0;
+      PieceIter<kGrouped, kSkip> it = it0;
       Piece pc{};
       int gi = 0, nbig = 0, nsmall = 0, gz = 0, npc = 0, empty_bar = 0;
       bool ok = true;
@@ -708,7 +717,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     const int row = L & 63, half = L >> 6;  // head within CTA; token half / latent half
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
     const float c2 = p.scale_log2;
-    PieceIter<kGrouped> it = it0;
+    PieceIter<kGrouped, kSkip> it = it0;
     Piece pc;
     int gi = 0, gz = 0, bbase = 0;  // bbase: big-slot uses before this piece
     while (it.next(p, pc)) {

@@ -578,9 +578,18 @@ struct Params {
   int n_tiles, N;      // 256-row tiles per batch, rows of X
   int kblk;            // K / 64
   __nv_bfloat16 *out0, *out1;  // [split][N][128] each
+  // k_gemm_resident<true> only: X row n is cache row (seq, n), found page by page
+  CacheView cache;
+  int seq, oob_row;            // oob_row: a row coordinate past the X map (zero fill)
+  __nv_bfloat16 *tail;         // [N][64]: the 64 columns after the K of each X row
 };
 }  // namespace rs
 
+// kGather = false: X is an array of N rows. kGather = true (the expansion of a
+// prefix): the rows are the first N positions of one cached sequence, fetched
+// as 64-row boxes whose row comes from the block table, and the columns after
+// c_KV (k_R) are copied to p.tail.
+template <bool kGather>
 __global__ void __launch_bounds__(rs::NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     k_gemm_resident(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
                     const __grid_constant__ CUtensorMap tm_x, const rs::Params p) {
@@ -625,6 +634,13 @@ __global__ void __launch_bounds__(rs::NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     if (lane == 0) {
       int na = 0, g = 0;
       bool ok = true;
+      [[maybe_unused]] int nt_rows = -1, box_row[2] = {0, 0};
+      [[maybe_unused]] auto gather_row = [&](int n) -> int {  // cache row of position n, or past the map
+        if (n >= p.N) return p.oob_row;
+        const int64_t row = cache_row(p.cache, p.seq, n);
+        if (row < 0) dev_error(MLA_DEVERR_DATA);
+        return row < 0 ? p.oob_row : static_cast<int>(row);
+      };
       for (int u = u0; u < u1 && ok; ++u) {
         const int bp = u / p.n_tiles, nt = u % p.n_tiles, b = 2 * bp + static_cast<int>(rank);
         if (pair_start(u)) {
@@ -642,8 +658,18 @@ __global__ void __launch_bounds__(rs::NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
           if (s % PRODUCERS != pid) continue;
           if (use > 0 && !(ok = mbar_wait(bar(rs::BAR_B_EMPTY + s), (use - 1) & 1, abort_flag))) break;
           if (rank == 0) mbar_arrive_expect_tx(bar(rs::BAR_B_FULL + s), 2 * rs::B_STAGE);
-          tma_load_2d_pair(sbase + rs::OFF_B + s * rs::B_STAGE, &tm_x, kb * BK, nt * rs::NT + rs::NHALF * rank,
-                           lead(rs::BAR_B_FULL + s));
+          if constexpr (!kGather) {
+            tma_load_2d_pair(sbase + rs::OFF_B + s * rs::B_STAGE, &tm_x, kb * BK, nt * rs::NT + rs::NHALF * rank,
+                             lead(rs::BAR_B_FULL + s));
+          } else {
+            if (nt != nt_rows) {  // this CTA's two 64-row boxes of the tile
+              nt_rows = nt;
+              for (int v = 0; v < 2; ++v) box_row[v] = gather_row(nt * rs::NT + rs::NHALF * static_cast<int>(rank) + 64 * v);
+            }
+            for (int v = 0; v < 2; ++v)
+              tma_load_2d_pair(sbase + rs::OFF_B + s * rs::B_STAGE + v * (rs::B_STAGE / 2), &tm_x, kb * BK, box_row[v],
+                               lead(rs::BAR_B_FULL + s));
+          }
         }
       }
       // drain: the releases of this producer's last slot uses and of the last A have arrived
@@ -690,6 +716,16 @@ __global__ void __launch_bounds__(rs::NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     const int cbeg = warp >= 8 ? rs::NT / 2 : 0;  // this warp's half of the tile's columns (tokens)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
     griddep_wait();  // outputs are written only once the previous kernel has finished
+    if constexpr (kGather) {  // the k_R columns, eight 16-byte words per row, while the first tiles load
+      const int e0 = static_cast<int>(blockIdx.x) * 32 * rs::EPI_WARPS + 32 * (warp >= 8 ? warp - 4 : warp - 2) + lane;
+      const int D8 = (64 * p.kblk + 64) / 8;
+      for (int64_t e = e0; e < 8ll * p.N; e += 32ll * rs::EPI_WARPS * gridDim.x) {
+        const int64_t row = cache_row(p.cache, p.seq, e >> 3);  // (a bad page is reported by the producers)
+        reinterpret_cast<uint4 *>(p.tail)[e] =
+            row < 0 ? make_uint4(0, 0, 0, 0)
+                    : static_cast<const uint4 *>(p.cache.data)[row * D8 + 8 * p.kblk + (e & 7)];
+      }
+    }
     int lt = 0;
     for (int u = u0; u < u1; ++u, ++lt) {
       const int bp = u / p.n_tiles, nt = u % p.n_tiles, b = 2 * bp + static_cast<int>(rank), buf = lt & 1;

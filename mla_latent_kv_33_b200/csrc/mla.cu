@@ -28,6 +28,8 @@
 #include "gemm_tc.cuh"
 #include "decode_tc.cuh"
 #include "prefill_tc.cuh"
+#include "prefix_tc.cuh"
+#include "paging.cuh"
 
 namespace {
 
@@ -88,7 +90,8 @@ mla_status launched(cudaError_t e, const char *what) {
 // cudaFuncSetAttribute applies to the current device: a kernel's dynamic
 // shared memory limit is raised once per device (bit `device` of its mask).
 enum SmemKernel {
-  SMEM_GEMM = 0, SMEM_ABSORB = 1, SMEM_DECODE = 2, SMEM_ATTEND_A = 3, SMEM_DECODE_NQ = 4, SMEM_GEMM_RES = 5, SMEM_KERNELS = 6
+  SMEM_GEMM = 0, SMEM_ABSORB = 1, SMEM_DECODE = 2, SMEM_ATTEND_A = 3, SMEM_DECODE_NQ = 4, SMEM_GEMM_RES = 5,
+  SMEM_EXPAND = 6, SMEM_DECODE_SUFFIX = 7, SMEM_DECODE_SUFFIX_NQ = 8, SMEM_PREFIX = 9, SMEM_PLAN = 10, SMEM_KERNELS = 11
 };
 std::atomic<uint64_t> g_smem_raised[SMEM_KERNELS];
 
@@ -915,10 +918,10 @@ mla_status tc_attend_a(const mla_dims *d, const void *qa, const void *W_UK, cons
     rp.out0 = kc;
     rp.out1 = vv;
     const int grid = 2 * std::max(1, std::min(sm_count() / 2, (rp.batches / 2) * rp.n_tiles));  // clusters of 2
-    if ((s = raise_smem_limit(reinterpret_cast<const void *>(G::k_gemm_resident), SMEM_GEMM_RES, G::rs::SMEM_BYTES,
+    if ((s = raise_smem_limit(reinterpret_cast<const void *>(G::k_gemm_resident<false>), SMEM_GEMM_RES, G::rs::SMEM_BYTES,
                               "decompression: set shared memory size")) != MLA_OK)
       return s;
-    if ((s = launched(launch_tc(G::k_gemm_resident, dim3(grid), dim3(G::rs::NUM_THREADS), G::rs::SMEM_BYTES, st, ta0,
+    if ((s = launched(launch_tc(G::k_gemm_resident<false>, dim3(grid), dim3(G::rs::NUM_THREADS), G::rs::SMEM_BYTES, st, ta0,
                                 ta1, tx, rp),
                       "order-A decompression (tensor cores)")) != MLA_OK)
       return s;
@@ -1059,7 +1062,7 @@ int decode_clusters(int sms) {
     if (c > 0) return std::min(c, sms / 2);
   }
   namespace D = mla::dec;
-  cudaFuncSetAttribute(D::k_decode<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, D::SMEM_BYTES);
+  cudaFuncSetAttribute(D::k_decode<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, D::SMEM_BYTES);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
   cfg.blockDim = dim3(D::NUM_THREADS, 1, 1);
@@ -1072,7 +1075,7 @@ int decode_clusters(int sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, D::k_decode<false>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, D::k_decode<false, false>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = sms / 2;
   }
@@ -1081,8 +1084,9 @@ int decode_clusters(int sms) {
   return n;
 }
 
+// skip > 0: attend to positions skip .. only (the suffix of a shared prefix).
 mla_status decode_tc(const mla_dims *d, const void *q, const mla_cache *c, const int32_t *seq_lens, int B, int n_q,
-                     void *o_lat, float *lse, int num_splits, void *ws, size_t ws_bytes, cudaStream_t st) {
+                     void *o_lat, float *lse, int num_splits, void *ws, size_t ws_bytes, cudaStream_t st, int skip = 0) {
   namespace D = mla::dec;
   const int BJ = B * n_q;
   if (BJ > D::MAX_UNITS) return fail(MLA_ERR_UNSUPPORTED, "tensor-core decode supports B*n_q <= %d", D::MAX_UNITS);
@@ -1143,10 +1147,14 @@ mla_status decode_tc(const mla_dims *d, const void *q, const mla_cache *c, const
   p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan_bytes);
   p.part_lse = p.part_o + slots * D::HEADS * D::DC;
 
+  p.skip = skip;
   // n_q > 1: the variant whose cluster groups follow the query positions
-  const auto kernel = n_q > 1 ? D::k_decode<true> : D::k_decode<false>;
-  if ((s = raise_smem_limit(reinterpret_cast<const void *>(kernel), n_q > 1 ? SMEM_DECODE_NQ : SMEM_DECODE,
-                            D::SMEM_BYTES, "decode: set shared memory size")) != MLA_OK)
+  const auto kernel = skip > 0 ? (n_q > 1 ? D::k_decode<true, true> : D::k_decode<false, true>)
+                               : (n_q > 1 ? D::k_decode<true, false> : D::k_decode<false, false>);
+  const SmemKernel which = skip > 0 ? (n_q > 1 ? SMEM_DECODE_SUFFIX_NQ : SMEM_DECODE_SUFFIX)
+                                    : (n_q > 1 ? SMEM_DECODE_NQ : SMEM_DECODE);
+  if ((s = raise_smem_limit(reinterpret_cast<const void *>(kernel), which, D::SMEM_BYTES,
+                            "decode: set shared memory size")) != MLA_OK)
     return s;
   if ((s = launched(launch_tc(kernel, dim3(2 * nclusters), dim3(D::NUM_THREADS), D::SMEM_BYTES, st, tm_q, tm_k, tm_v[0],
                               tm_v[1], p),
@@ -1154,6 +1162,217 @@ mla_status decode_tc(const mla_dims *d, const void *q, const mla_cache *c, const
     return s;
   return launched(launch_tc(D::k_combine, dim3(BJ * D::COMBINE_BLOCKS_PER_ROW), dim3(128), 0, st, p),
                   "decode combine");
+}
+
+// ---------------------------------------- shared prefix: expansion, decode --
+
+// kc, v [n_h][P][d_h] and kr [P][d_r] of the first P positions of one cached
+// sequence, on SM pairs: the order-A decompression over gathered cache rows.
+mla_status tc_prefix_expand(const mla_dims *d, const mla_cache *c, int seq, int P, const void *W_UK, const void *W_UV,
+                            void *kc, void *v, void *kr, cudaStream_t st) {
+  const int64_t R = cache_rows_of(c), D = d->d_c + d->d_r;
+  if (c->paged && c->block_size % 64 != 0)
+    return fail(MLA_ERR_UNSUPPORTED, "prefix_expand needs block_size to be a multiple of 64");
+  if (R >= 0x7fff0000LL) return fail(MLA_ERR_UNSUPPORTED, "prefix_expand: too many cache rows for 32-bit coordinates");
+  const int HD = d->n_h * d->d_h;
+  CUtensorMap ta0, ta1, tx;
+  mla_status s;
+  if ((s = make_tmap_bf16(&tx, c->data, d->d_c, R, D * 2, 64, 64, "cache (c_KV)")) != MLA_OK) return s;
+  if ((s = make_tmap_bf16(&ta0, W_UK, d->d_c, HD, d->d_c * 2ull, 64, 128, "W_UK")) != MLA_OK) return s;
+  if ((s = make_tmap_bf16(&ta1, W_UV, d->d_c, HD, d->d_c * 2ull, 64, 128, "W_UV")) != MLA_OK) return s;
+  G::rs::Params rp{};
+  rp.batches = 2 * d->n_h;
+  rp.split = d->n_h;
+  rp.n_tiles = (P + G::rs::NT - 1) / G::rs::NT;
+  rp.N = P;
+  rp.kblk = d->d_c / G::BK;
+  rp.out0 = static_cast<__nv_bfloat16 *>(kc);
+  rp.out1 = static_cast<__nv_bfloat16 *>(v);
+  rp.cache = view_of(c);
+  rp.seq = seq;
+  rp.oob_row = static_cast<int>(R);
+  rp.tail = static_cast<__nv_bfloat16 *>(kr);
+  const int64_t units = static_cast<int64_t>(d->n_h) * rp.n_tiles;
+  const int grid = 2 * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count() / 2, units)));
+  if ((s = raise_smem_limit(reinterpret_cast<const void *>(G::k_gemm_resident<true>), SMEM_EXPAND, G::rs::SMEM_BYTES,
+                            "prefix expansion: set shared memory size")) != MLA_OK)
+    return s;
+  return launched(launch_tc(G::k_gemm_resident<true>, dim3(grid), dim3(G::rs::NUM_THREADS), G::rs::SMEM_BYTES, st, ta0,
+                            ta1, tx, rp),
+                  "prefix expansion (tensor cores)");
+}
+
+template <typename T>
+mla_status simt_prefix_expand(const mla_dims *d, const mla_cache *c, int seq, int P, const void *W_UK, const void *W_UV,
+                              void *kc, void *v, void *kr, cudaStream_t st) {
+  MLA_LAUNCH(mla::k_simt_expand<T><<<(P + 3) / 4, 256, 4 * d->d_c * sizeof(float), st>>>(
+      view_of(c), seq, P, static_cast<const T *>(W_UK), static_cast<const T *>(W_UV), d->n_h, d->d_h, d->d_c, d->d_r,
+      static_cast<T *>(kc), static_cast<T *>(v), static_cast<T *>(kr)));
+  return cuda_check("prefix expansion (CUDA cores)");
+}
+
+// Workspace of a shared-prefix decode: absorbed queries, the suffix's latent
+// readout, its lse and its W_UV readout, the prefix partials, and the suffix
+// decode's own workspace.
+struct SharedPlan {
+  int T, nt, units, ctas, part_rows;
+  size_t q, o_lat, lse_s, o_s, part_o, part_lse, dec, total;
+};
+
+SharedPlan shared_plan(const mla_dims *d, int B, int n_q, int64_t P) {
+  namespace X = mla::pfx;
+  SharedPlan w{};
+  const size_t T = static_cast<size_t>(B) * n_q, H = d->n_h;
+  const int sms = sm_count();
+  w.T = B * n_q;
+  w.nt = static_cast<int>((P + X::KTILE - 1) / X::KTILE);
+  w.units = (w.T + X::QROWS - 1) / X::QROWS * d->n_h;
+  w.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, static_cast<int64_t>(w.units) * w.nt)));
+  w.part_rows = std::min(w.T, static_cast<int>(X::QROWS));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align256(bytes);
+    return o;
+  };
+  w.q = take(T * H * (d->d_c + d->d_r) * 2);
+  w.o_lat = take(T * H * d->d_c * 2);
+  w.lse_s = take(T * H * sizeof(float));
+  w.o_s = take(T * H * d->d_h * 2);
+  const size_t slots = P > 0 ? static_cast<size_t>(w.units) + w.ctas : 0;
+  w.part_o = take(slots * w.part_rows * d->d_h * sizeof(float));
+  w.part_lse = take(slots * w.part_rows * sizeof(float));
+  w.dec = at;
+  w.total = at + mla::decode_tc_ws(B, n_q, sms);
+  return w;
+}
+
+size_t simt_shared_ws(const mla_dims *d, int T) {  // q_lat, fp32
+  return sizeof(float) * static_cast<size_t>(T) * d->n_h * d->d_c;
+}
+
+mla_status tc_decode_shared(const mla_dims *d, const void *qa, const void *kc, const void *v, const void *kr, int P,
+                            const mla_cache *c, const int32_t *seq_lens, int B, int n_q, const void *W_UK,
+                            const void *W_UV, void *o, float *lse, void *ws, size_t ws_bytes, cudaStream_t st) {
+  namespace X = mla::pfx;
+  if (c->paged && P % 64 != 0)
+    return fail(MLA_ERR_UNSUPPORTED, "decode_shared needs prefix_len to be a multiple of 64 on a paged cache");
+  const SharedPlan w = shared_plan(d, B, n_q, P);
+  uint8_t *w8 = static_cast<uint8_t *>(ws);
+  __nv_bfloat16 *q = reinterpret_cast<__nv_bfloat16 *>(w8 + w.q), *o_lat = reinterpret_cast<__nv_bfloat16 *>(w8 + w.o_lat),
+                *o_s = reinterpret_cast<__nv_bfloat16 *>(w8 + w.o_s);
+  float *lse_s = reinterpret_cast<float *>(w8 + w.lse_s);
+  const int T = w.T, HD = d->n_h * d->d_h, HQ = d->n_h * X::DQK;
+  mla_status s;
+  // prefix attention, and q_R into the absorbed queries
+  CUtensorMap tm_q, tm_kc, tm_kr, tm_v;
+  {
+    const uint64_t dims[3] = {static_cast<uint64_t>(X::DQK), static_cast<uint64_t>(d->n_h), static_cast<uint64_t>(T)};
+    const uint64_t str[2] = {X::DQK * 2ull, static_cast<uint64_t>(d->n_h) * X::DQK * 2};
+    const uint32_t box[3] = {64, 1, X::QROWS};
+    if ((s = make_tmap_nd(&tm_q, qa, 3, dims, str, box, "qa")) != MLA_OK) return s;
+  }
+  tm_kc = tm_kr = tm_v = tm_q;  // P = 0: nothing is loaded
+  if (P > 0) {
+    for (int u = 0; u < 2; ++u) {
+      const uint64_t dims[3] = {static_cast<uint64_t>(d->d_h), static_cast<uint64_t>(P), static_cast<uint64_t>(d->n_h)};
+      const uint64_t str[2] = {d->d_h * 2ull, static_cast<uint64_t>(P) * d->d_h * 2};
+      const uint32_t box[3] = {64, X::KTILE, 1};
+      if ((s = make_tmap_nd(u == 0 ? &tm_kc : &tm_v, u == 0 ? kc : v, 3, dims, str, box, u == 0 ? "kc" : "v")) != MLA_OK)
+        return s;
+    }
+    if ((s = make_tmap_bf16(&tm_kr, kr, d->d_r, P, d->d_r * 2ull, 64, X::KTILE, "kr")) != MLA_OK) return s;
+  }
+  X::Params xp{};
+  xp.T = T;
+  xp.P = P;
+  xp.nt = w.nt;
+  xp.units = w.units;
+  xp.part_rows = w.part_rows;
+  xp.scale = softmax_scale(d);
+  xp.scale_log2 = xp.scale * 1.4426950408889634f;
+  xp.part_o = reinterpret_cast<float *>(w8 + w.part_o);
+  xp.part_lse = reinterpret_cast<float *>(w8 + w.part_lse);
+  xp.qa = static_cast<const __nv_bfloat16 *>(qa);
+  xp.q = q;
+  if ((s = raise_smem_limit(reinterpret_cast<const void *>(X::k_prefix_attend), SMEM_PREFIX, X::SMEM_BYTES,
+                            "prefix attention: set shared memory size")) != MLA_OK)
+    return s;
+  if ((s = launched(launch_tc(X::k_prefix_attend, dim3(w.ctas), dim3(X::NUM_THREADS), X::SMEM_BYTES, st, tm_q, tm_kc,
+                              tm_kr, tm_v, xp),
+                    "prefix attention (tensor cores)")) != MLA_OK)
+    return s;
+  // q_lat,h = W_UK_h^T q_C,h, straight from qa (the q_C columns of head h)
+  {
+    const int64_t Dq = d->d_c + d->d_r;
+    const GemmShape g = gemm_shape(d->d_c, T, d->d_h, d->n_h, false);
+    CUtensorMap ta, tb;
+    if ((s = make_tmap_bf16(&ta, W_UK, d->d_c, HD, d->d_c * 2ull, 64, 64, "W_UK")) != MLA_OK) return s;
+    if ((s = make_tmap_bf16(&tb, qa, HQ, T, HQ * 2ull, 64, g.n_tile, "qa (q_C)")) != MLA_OK) return s;
+    G::Params p{};
+    p.epi = G::EPI_BF16;
+    p.dst = q;
+    p.e_bs = Dq;
+    p.e_ns = d->n_h * Dq;
+    GemmOperands op = operands(ta, tb);
+    op.a_mn_major = true;
+    op.a_batch_rows = d->d_h;
+    op.b_batch_cols = X::DQK;
+    if ((s = launch_gemm(op, g, T, p, st)) != MLA_OK) return s;
+  }
+  // the suffix, absorbed, and its W_UV readout
+  if ((s = decode_tc(d, q, c, seq_lens, B, n_q, o_lat, lse_s, 0, w8 + w.dec, ws_bytes - w.dec, st, P)) != MLA_OK) return s;
+  if ((s = tc_out_proj(d, o_lat, W_UV, T, o_s, nullptr, st)) != MLA_OK) return s;
+  X::MergeParams mp{};
+  mp.T = T;
+  mp.n_q = n_q;
+  mp.P = P;
+  mp.nt = w.nt;
+  mp.units = w.units;
+  mp.part_rows = w.part_rows;
+  mp.ctas = w.ctas;
+  mp.capacity = cache_capacity(c);
+  mp.seq_lens = seq_lens;
+  mp.part_o = xp.part_o;
+  mp.part_lse = xp.part_lse;
+  mp.o_s = o_s;
+  mp.lse_s = lse_s;
+  mp.o = static_cast<__nv_bfloat16 *>(o);
+  mp.lse = lse;
+  const int64_t warps = static_cast<int64_t>(T) * d->n_h;
+  return launched(launch_tc(X::k_merge_shared, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, st, mp),
+                  "shared-prefix merge");
+}
+
+template <typename T>
+mla_status simt_decode_shared(const mla_dims *d, const void *qa, const void *kc, const void *v, const void *kr, int P,
+                              const mla_cache *c, const int32_t *seq_lens, int B, int n_q, const void *W_UK,
+                              const void *W_UV, void *o, float *lse, void *ws, cudaStream_t st) {
+  const int64_t HQ = static_cast<int64_t>(d->n_h) * (d->d_h + d->d_r), HC = static_cast<int64_t>(d->n_h) * d->d_c;
+  float *q_lat = static_cast<float *>(ws);  // [T][n_h][d_c]
+  // q_lat,h[j] = sum_i W_UK[h*d_h + i][j] q_C,h[i]: batch = head, W(h, n=j, k=i)
+  launch_linear<T>(static_cast<const T *>(W_UK), static_cast<int64_t>(d->d_h) * d->d_c, 1, d->d_c, qa, false,
+                   d->d_h + d->d_r, HQ, q_lat, d->d_c, HC, d->d_c, d->d_h, B * n_q, d->n_h, st);
+  const size_t smem = sizeof(float) * (d->d_h + d->d_r + 2 * static_cast<size_t>(d->d_c));
+  MLA_LAUNCH(mla::k_simt_shared<T><<<B * n_q * d->n_h, 256, smem, st>>>(
+      static_cast<const T *>(qa), q_lat, static_cast<const T *>(kc), static_cast<const T *>(v),
+      static_cast<const T *>(kr), P, view_of(c), seq_lens, n_q, d->n_h, d->d_h, d->d_c, d->d_r, softmax_scale(d),
+      static_cast<const T *>(W_UV), static_cast<T *>(o), lse));
+  return cuda_check("shared-prefix decode (CUDA cores)");
+}
+
+// ------------------------------------------------ block tables, slot writes --
+
+template <typename V>
+mla_status cache_write(const void *rows, const int64_t *slots, int T, const mla_cache *c, size_t row_bytes,
+                       cudaStream_t st) {
+  const int vec = static_cast<int>(row_bytes / sizeof(V));
+  const int64_t n = static_cast<int64_t>(T) * vec;
+  // a thread copies four words; at most eight blocks of 256 threads per SM
+  const int64_t blocks = std::min<int64_t>((n + 4 * 256 - 1) / (4 * 256), 8ll * sm_count());
+  return launched(launch_tc(mla::page::k_cache_write<V>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
+                            static_cast<const V *>(rows), slots, static_cast<V *>(c->data), cache_rows_of(c), n, vec),
+                  "cache write");
 }
 
 }  // namespace
@@ -1253,7 +1472,7 @@ int32_t mla_get_launch_overlap(void) { return g_overlap.load(std::memory_order_r
 
 int32_t mla_uses_tensor_cores(const mla_dims *d, int32_t op) {
   if (d == nullptr || !tc_geometry(d)) return 0;
-  return (op >= MLA_OP_APPEND && op <= MLA_OP_ATTEND_A) ? 1 : 0;
+  return (op >= MLA_OP_APPEND && op <= MLA_OP_DECODE_SHARED) ? 1 : 0;
 }
 
 size_t mla_workspace_size(const mla_dims *d, int32_t op, int32_t rows, int32_t n_q, int64_t max_seq_len,
@@ -1273,6 +1492,12 @@ size_t mla_workspace_size(const mla_dims *d, int32_t op, int32_t rows, int32_t n
       return tc ? tc_front_ws(d, rows) : std::max(simt_append_ws(d, rows), simt_absorb_ws(d, rows));
     case MLA_OP_QUERY_HEADS: return tc ? tc_query_heads_ws(d, rows) : simt_query_heads_ws(d, rows);
     case MLA_OP_ATTEND_A: return tc && max_seq_len > 0 ? tc_attend_a_ws(d, max_seq_len) : 0;
+    case MLA_OP_PREFIX_EXPAND: return 0;
+    case MLA_OP_DECODE_SHARED: {
+      const int64_t T = static_cast<int64_t>(rows) * (n_q < 1 ? 1 : n_q);
+      if (T > mla::dec::MAX_UNITS || max_seq_len < 0 || max_seq_len > INT32_MAX) return 0;
+      return tc ? shared_plan(d, rows, n_q < 1 ? 1 : n_q, max_seq_len).total : simt_shared_ws(d, static_cast<int>(T));
+    }
   }
   return 0;
 }
@@ -1520,6 +1745,119 @@ mla_status mla_attend_order_a(const mla_dims *d, const void *qa, const void *W_U
   if (tc_geometry(d)) return tc_attend_a(d, qa, W_UK, W_UV, c, seq_lens, B, n_q, o, ws, st);
   if (d->dtype == MLA_BF16) return simt_attend_a<__nv_bfloat16>(d, qa, W_UK, W_UV, c, seq_lens, B, n_q, o, st);
   return simt_attend_a<float>(d, qa, W_UK, W_UV, c, seq_lens, B, n_q, o, st);
+}
+
+mla_status mla_batch_plan(const mla_cache *c, int32_t *block_table, const int32_t *ctx_lens, const int32_t *new_lens,
+                          int32_t B, const int32_t *free_blocks, int32_t num_free, const int32_t *shared_blocks,
+                          int32_t num_shared, int32_t T, int32_t *seq_lens, int32_t *row_start, int32_t *seq_idx,
+                          int32_t *positions, int64_t *slots, int32_t *used, void *stream) {
+  namespace N = mla::page;
+  if (c == nullptr) return fail(MLA_ERR_INVALID_ARG, "batch_plan: cache is NULL");
+  if (!c->paged) return fail(MLA_ERR_INVALID_ARG, "batch_plan: the cache must be paged");
+  if (c->block_size <= 0 || c->max_blocks_per_seq <= 0 || c->num_blocks <= 0)
+    return fail(MLA_ERR_INVALID_ARG, "paged cache needs block_size, max_blocks_per_seq, num_blocks > 0");
+  if (B <= 0 || T <= 0) return fail(MLA_ERR_INVALID_ARG, "batch_plan: B and T must be positive");
+  if (B > c->num_seqs) return fail(MLA_ERR_INVALID_ARG, "B exceeds cache->num_seqs");
+  if (num_free < 0 || num_shared < 0) return fail(MLA_ERR_INVALID_ARG, "batch_plan: num_free and num_shared must be >= 0");
+  if (num_shared > c->max_blocks_per_seq)
+    return fail(MLA_ERR_INVALID_ARG, "batch_plan: num_shared exceeds cache->max_blocks_per_seq");
+  if (!block_table || !ctx_lens || (num_free && !free_blocks) || (num_shared && !shared_blocks) || !seq_lens ||
+      !row_start || !seq_idx || !positions || !slots || !used)
+    return fail(MLA_ERR_INVALID_ARG, "batch_plan: NULL tensor argument");
+  if (B > N::MAX_REQUESTS) return fail(MLA_ERR_UNSUPPORTED, "batch_plan serves at most %d requests", N::MAX_REQUESTS);
+  N::PlanParams p{};
+  p.ctx_lens = ctx_lens;
+  p.new_lens = new_lens;
+  p.free_blocks = free_blocks;
+  p.shared_blocks = shared_blocks;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.row_start = row_start;
+  p.seq_idx = seq_idx;
+  p.positions = positions;
+  p.used = used;
+  p.slots = slots;
+  p.num_blocks = c->num_blocks;
+  p.B = B;
+  p.T = T;
+  p.num_free = num_free;
+  p.num_shared = num_shared;
+  p.block_size = c->block_size;
+  p.max_blocks = c->max_blocks_per_seq;
+  mla_status s = raise_smem_limit(reinterpret_cast<const void *>(N::k_batch_plan), SMEM_PLAN,
+                                  2 * N::MAX_REQUESTS * static_cast<int>(sizeof(int32_t)),
+                                  "batch plan: set shared memory size");
+  if (s != MLA_OK) return s;
+  const int64_t items = std::max<int64_t>(T, static_cast<int64_t>(B) * num_shared);
+  const int64_t blocks = std::min<int64_t>((items + 2 * N::PLAN_THREADS - 1) / (2 * N::PLAN_THREADS), sm_count());
+  return launched(launch_tc(N::k_batch_plan, dim3(static_cast<unsigned>(blocks)), dim3(N::PLAN_THREADS),
+                            2 * sizeof(int32_t) * B, static_cast<cudaStream_t>(stream), p),
+                  "batch plan");
+}
+
+mla_status mla_cache_write(const mla_dims *d, const void *rows, const int64_t *slots, int32_t T, const mla_cache *c,
+                           void *stream) {
+  mla_status s = check_dims(d);
+  if (s != MLA_OK) return s;
+  if (T <= 0) return fail(MLA_ERR_INVALID_ARG, "T must be positive");
+  if (!rows || !slots) return fail(MLA_ERR_INVALID_ARG, "cache_write: NULL tensor argument");
+  if (!aligned16(rows)) return fail(MLA_ERR_INVALID_ARG, "cache_write: rows must be 16-byte aligned");
+  if ((s = check_cache(c, d->d_c + d->d_r)) != MLA_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // the widest word that divides a row: 16 bytes for every usual width
+  const size_t row_bytes = static_cast<size_t>(d->d_c + d->d_r) * elem_size(d);
+  if (row_bytes % 16 == 0) return cache_write<uint4>(rows, slots, T, c, row_bytes, st);
+  if (row_bytes % 4 == 0) return cache_write<uint32_t>(rows, slots, T, c, row_bytes, st);
+  return cache_write<uint16_t>(rows, slots, T, c, row_bytes, st);
+}
+
+mla_status mla_prefix_expand(const mla_dims *d, const mla_cache *c, int32_t seq, int32_t prefix_len, const void *W_UK,
+                             const void *W_UV, void *kc, void *v, void *kr, void *stream) {
+  mla_status s = check_dims(d);
+  if (s != MLA_OK) return s;
+  if (prefix_len <= 0) return fail(MLA_ERR_INVALID_ARG, "prefix_expand: prefix_len must be positive");
+  if (!W_UK || !W_UV || !kc || !v || !kr) return fail(MLA_ERR_INVALID_ARG, "prefix_expand: NULL tensor argument");
+  if (!aligned16(W_UK) || !aligned16(W_UV) || !aligned16(kc) || !aligned16(v) || !aligned16(kr))
+    return fail(MLA_ERR_INVALID_ARG, "prefix_expand: tensors must be 16-byte aligned");
+  if ((s = check_cache(c, d->d_c + d->d_r)) != MLA_OK) return s;
+  if (seq < 0 || seq >= c->num_seqs) return fail(MLA_ERR_INVALID_ARG, "prefix_expand: seq is not a sequence of the cache");
+  if (prefix_len > cache_capacity(c)) return fail(MLA_ERR_INVALID_ARG, "prefix_expand: prefix_len exceeds the cache's capacity");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tc_geometry(d)) return tc_prefix_expand(d, c, seq, prefix_len, W_UK, W_UV, kc, v, kr, st);
+  if (d->dtype == MLA_BF16)
+    return simt_prefix_expand<__nv_bfloat16>(d, c, seq, prefix_len, W_UK, W_UV, kc, v, kr, st);
+  return simt_prefix_expand<float>(d, c, seq, prefix_len, W_UK, W_UV, kc, v, kr, st);
+}
+
+mla_status mla_decode_shared(const mla_dims *d, const void *qa, const void *kc, const void *v, const void *kr,
+                             int32_t prefix_len, const mla_cache *c, const int32_t *seq_lens, int32_t B, int32_t n_q,
+                             const void *W_UK, const void *W_UV, void *o, float *lse, void *ws, size_t ws_bytes,
+                             void *stream) {
+  mla_status s = check_dims(d);
+  if (s != MLA_OK) return s;
+  if (B <= 0 || n_q <= 0) return fail(MLA_ERR_INVALID_ARG, "B and n_q must be positive");
+  if (prefix_len < 0) return fail(MLA_ERR_INVALID_ARG, "decode_shared: prefix_len must be >= 0");
+  if (!qa || !seq_lens || !W_UK || !W_UV || !o || (prefix_len > 0 && (!kc || !v || !kr)))
+    return fail(MLA_ERR_INVALID_ARG, "decode_shared: NULL tensor argument");
+  if (!aligned16(qa) || !aligned16(kc) || !aligned16(v) || !aligned16(kr) || !aligned16(W_UK) || !aligned16(W_UV) ||
+      !aligned16(o))
+    return fail(MLA_ERR_INVALID_ARG, "decode_shared: tensors must be 16-byte aligned");
+  if ((s = check_cache(c, d->d_c + d->d_r)) != MLA_OK) return s;
+  if (B > c->num_seqs) return fail(MLA_ERR_INVALID_ARG, "B exceeds cache->num_seqs");
+  if (static_cast<int64_t>(prefix_len) + n_q > cache_capacity(c))
+    return fail(MLA_ERR_INVALID_ARG, "decode_shared: prefix_len + n_q exceeds the cache's capacity");
+  if (static_cast<int64_t>(B) * n_q > mla::dec::MAX_UNITS)
+    return fail(MLA_ERR_UNSUPPORTED, "decode_shared supports B*n_q <= %d", mla::dec::MAX_UNITS);
+  if (d->d_h > 256) return fail(MLA_ERR_UNSUPPORTED, "decode_shared: d_h must be <= 256");
+  const size_t need = mla_workspace_size(d, MLA_OP_DECODE_SHARED, B, n_q, prefix_len, 0);
+  if (ws_bytes < need || (need && !ws)) return fail(MLA_ERR_WORKSPACE, "decode_shared needs %zu workspace bytes", need);
+  if (!aligned16(ws)) return fail(MLA_ERR_INVALID_ARG, "decode_shared: ws must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tc_geometry(d))
+    return tc_decode_shared(d, qa, kc, v, kr, prefix_len, c, seq_lens, B, n_q, W_UK, W_UV, o, lse, ws, ws_bytes, st);
+  if (d->dtype == MLA_BF16)
+    return simt_decode_shared<__nv_bfloat16>(d, qa, kc, v, kr, prefix_len, c, seq_lens, B, n_q, W_UK, W_UV, o, lse, ws, st);
+  return simt_decode_shared<float>(d, qa, kc, v, kr, prefix_len, c, seq_lens, B, n_q, W_UK, W_UV, o, lse, ws, st);
 }
 
 mla_status mla_selftest_timeout(uint64_t wait_ns, void *scratch, size_t scratch_bytes, void *stream) {

@@ -245,4 +245,192 @@ __global__ void __launch_bounds__(256) k_simt_decode(const T *__restrict__ q, Ca
   if (lse != nullptr && threadIdx.x == 0) lse[static_cast<int64_t>(t) * n_h + h] = M + logf(Lsum);
 }
 
+// Expansion of a prefix (MLA walk-through, section 3 order A): for position
+// i < P of cached sequence seq, kc[h][i] = W_UK_h c_KV_i, v[h][i] = W_UV_h
+// c_KV_i, kr[i] = k_R,i. Four positions per block share every weight row read;
+// a warp forms one output row at a time. A position without a cache row reads
+// as zeros. Dynamic shared memory: 4 d_c floats.
+template <typename T>
+__global__ void __launch_bounds__(256) k_simt_expand(CacheView cache, int seq, int P, const T *__restrict__ W_UK,
+                                                     const T *__restrict__ W_UV, int n_h, int d_h, int d_c, int d_r,
+                                                     T *__restrict__ kc, T *__restrict__ v, T *__restrict__ kr) {
+  constexpr int NT = 4;
+  extern __shared__ float c_s[];  // [NT][d_c]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i0 = blockIdx.x * NT, D = d_c + d_r;
+  for (int u = 0; u < NT; ++u) {
+    const int i = i0 + u;
+    const int64_t row = i < P ? cache_row(cache, seq, i) : -1;
+    if (i < P && row < 0 && threadIdx.x == 0) dev_error(MLA_DEVERR_DATA);
+    const T *src = static_cast<const T *>(cache.data) + (row < 0 ? 0 : row) * D;
+    for (int e = threadIdx.x; e < D; e += 256) {
+      const T x = row < 0 ? from_f<T>(0.f) : src[e];
+      if (e < d_c) c_s[u * d_c + e] = ld_f(&x);
+      else if (i < P) kr[static_cast<int64_t>(i) * d_r + e - d_c] = x;
+    }
+  }
+  __syncthreads();
+  const int HD = n_h * d_h;
+  for (int o = warp; o < 2 * HD; o += 8) {
+    const int m = o < HD ? o : o - HD;
+    const T *w = (o < HD ? W_UK : W_UV) + static_cast<int64_t>(m) * d_c;
+    float acc[NT] = {0.f, 0.f, 0.f, 0.f};
+    for (int e = lane; e < d_c; e += 32) {
+      const float x = ld_f(w + e);
+#pragma unroll
+      for (int u = 0; u < NT; ++u) acc[u] += x * c_s[u * d_c + e];
+    }
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) acc[u] += __shfl_xor_sync(0xffffffffu, acc[u], k);
+    const int h = m / d_h, k = m % d_h;
+    T *dst = o < HD ? kc : v;
+    if (lane < NT && i0 + lane < P) {
+      const float x = lane == 0 ? acc[0] : (lane == 1 ? acc[1] : (lane == 2 ? acc[2] : acc[3]));
+      dst[(static_cast<int64_t>(h) * P + i0 + lane) * d_h + k] = from_f<T>(x);
+    }
+  }
+}
+
+// Shared-prefix decode, one block per (token row t, head h): one online
+// softmax over the P expanded prefix keys (score qa . [kc ; kr], value v) and
+// the row's visible suffix positions P .. (score q_lat . c_KV + q_R . k_R,
+// value c_KV, taken through W_UV at the end). Keys go in chunks of 256: eight
+// lanes form a score, then the threads, as `slices` groups of `width` output
+// columns, add the chunk's weighted values. fp32 throughout; q_lat [T][n_h][d_c]
+// fp32. Dynamic shared memory: (d_h + d_r) + 2 d_c floats.
+template <typename T>
+__global__ void __launch_bounds__(256) k_simt_shared(const T *__restrict__ qa, const float *__restrict__ q_lat,
+                                                     const T *__restrict__ kc, const T *__restrict__ v,
+                                                     const T *__restrict__ kr, int P, CacheView cache,
+                                                     const int32_t *__restrict__ seq_lens, int n_q, int n_h, int d_h,
+                                                     int d_c, int d_r, float scale, const T *__restrict__ W_UV,
+                                                     T *__restrict__ o, float *__restrict__ lse) {
+  constexpr int NT = 256, MAXC = 4;  // d_c <= 1024, d_h <= 256
+  extern __shared__ float sh[];
+  float *q_s = sh, *ql_s = sh + d_h + d_r, *oc_s = ql_s + d_c;
+  __shared__ float p_s[NT], r_s[NT / 32], x_s[NT];
+  __shared__ int64_t row_s[NT];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t = blockIdx.x / n_h, h = blockIdx.x % n_h, b = t / n_q, j = t % n_q, D = d_c + d_r;
+  const int64_t cap = cache.paged ? static_cast<int64_t>(cache.max_blocks_per_seq) * cache.block_size : cache.max_len;
+  const int L = seq_lens[b];
+  if (static_cast<int64_t>(L) < static_cast<int64_t>(P) + n_q || L > cap) {
+    if (tid == 0 && h == 0 && j == 0) dev_error(MLA_DEVERR_DATA);
+    return;
+  }
+  const int total = L - n_q + 1 + j;  // visible positions, the prefix's P first
+  const int64_t th = static_cast<int64_t>(t) * n_h + h;
+  for (int e = tid; e < d_h + d_r; e += NT) q_s[e] = ld_f(qa + th * (d_h + d_r) + e);
+  for (int e = tid; e < d_c; e += NT) ql_s[e] = q_lat[th * d_c + e];
+  const T *data = static_cast<const T *>(cache.data);
+  auto pow2 = [](int n) {
+    int w = 32;
+    while (w < n && w < NT) w <<= 1;
+    return w;
+  };
+  const int wv = pow2(d_h), wc = pow2(d_c);
+  float m = -INFINITY, l = 0.f, av = 0.f, ac[MAXC] = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < total;) {
+    const bool pre = k0 < P;
+    const int n = min(NT, (pre ? P : total) - k0);
+    __syncthreads();  // q staged, and the last chunk's scores and rows no longer read
+    if (!pre && tid < n) {
+      const int64_t row = cache_row(cache, b, k0 + tid);
+      if (row < 0) dev_error(MLA_DEVERR_DATA);  // reads as a row of zeros
+      row_s[tid] = row;
+    }
+    __syncthreads();
+    const int sub = tid >> 3, l8 = tid & 7;
+    float mx = -INFINITY;
+    for (int i = sub; i < (n + 3) / 4 * 4; i += NT / 8) {  // the four keys of a warp go round together
+      float s = 0.f;
+      if (i < n) {
+        if (pre) {
+          const T *k = kc + (static_cast<int64_t>(h) * P + k0 + i) * d_h, *kx = kr + static_cast<int64_t>(k0 + i) * d_r;
+          for (int e = l8; e < d_h; e += 8) s += q_s[e] * ld_f(k + e);
+          for (int e = l8; e < d_r; e += 8) s += q_s[d_h + e] * ld_f(kx + e);
+        } else if (row_s[i] >= 0) {
+          const T *k = data + row_s[i] * D;
+          for (int e = l8; e < d_c; e += 8) s += ql_s[e] * ld_f(k + e);
+          for (int e = l8; e < d_r; e += 8) s += q_s[d_h + e] * ld_f(k + d_c + e);
+        }
+      }
+#pragma unroll
+      for (int w = 4; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+      s *= scale;
+      if (i < n) {
+        mx = fmaxf(mx, s);
+        if (l8 == 0) p_s[i] = s;
+      }
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    if (lane == 0) r_s[warp] = mx;
+    __syncthreads();
+    float mn = m;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, r_s[w]);
+    const float alpha = __expf(m - mn);  // m = -inf on the first chunk: 0
+    m = mn;
+    float pv = 0.f;
+    if (tid < n) pv = p_s[tid] = __expf(p_s[tid] - m);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) pv += __shfl_xor_sync(0xffffffffu, pv, w);
+    __syncthreads();
+    if (lane == 0) r_s[warp] = pv;
+    __syncthreads();
+    l *= alpha;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) l += r_s[w];
+    av *= alpha;
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c) ac[c] *= alpha;
+    if (pre) {
+      const int e = tid % wv;
+      if (e < d_h)
+        for (int i = tid / wv; i < n; i += NT / wv)
+          av += p_s[i] * ld_f(v + (static_cast<int64_t>(h) * P + k0 + i) * d_h + e);
+    } else {
+      for (int i = tid / wc; i < n; i += NT / wc) {
+        if (row_s[i] < 0) continue;
+        const float pi = p_s[i];
+        const T *k = data + row_s[i] * D;
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c)
+          if (tid % wc + c * wc < d_c) ac[c] += pi * ld_f(k + tid % wc + c * wc);
+      }
+    }
+    k0 += n;
+  }
+  // sum the slices: the suffix's latent readout, then the prefix's values
+#pragma unroll
+  for (int c = 0; c < MAXC; ++c) {
+    __syncthreads();
+    x_s[tid] = ac[c];
+    __syncthreads();
+    const int e = tid + c * wc;
+    if (tid < wc && e < d_c) {
+      float s = 0.f;
+      for (int k = tid; k < NT; k += wc) s += x_s[k];
+      oc_s[e] = s;
+    }
+  }
+  __syncthreads();
+  x_s[tid] = av;
+  __syncthreads();
+  const float inv = 1.f / l;
+  for (int k = warp; k < d_h; k += NT / 32) {
+    const T *w = W_UV + (static_cast<int64_t>(h) * d_h + k) * d_c;
+    float s = 0.f;
+    for (int e = lane; e < d_c; e += 32) s += ld_f(w + e) * oc_s[e];
+    for (int e = k + lane * wv; e < NT; e += 32 * wv) s += x_s[e];
+#pragma unroll
+    for (int u = 16; u > 0; u >>= 1) s += __shfl_xor_sync(0xffffffffu, s, u);
+    if (lane == 0) o[th * d_h + k] = from_f<T>(s * inv);
+  }
+  if (lse != nullptr && tid == 0) lse[th] = m + logf(l);
+}
+
 }  // namespace mla

@@ -24,7 +24,7 @@ MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_WORKSPACE, MLA_ERR_CUD
     MLA_ERR_DEVICE_DATA = range(7)
 MLA_BF16, MLA_FP32 = 0, 1
 OP_APPEND, OP_ABSORB, OP_DECODE, OP_OUT_PROJ, OP_O_PROJ, OP_O_PROJ_LATENT, OP_ABSORB_MERGED, OP_FRONT_END, \
-    OP_ABSORB_WO, OP_QUERY_HEADS, OP_ATTEND_A = range(11)
+    OP_ABSORB_WO, OP_QUERY_HEADS, OP_ATTEND_A, OP_PREFIX_EXPAND, OP_DECODE_SHARED = range(13)
 
 
 class Dims(C.Structure):
@@ -58,6 +58,12 @@ _lib.mla_selftest_timeout.argtypes = [C.c_uint64, _P, _S, _P]
 _lib.mla_query_heads.argtypes = [C.POINTER(Dims), _P, _P, _P, _P, _P, C.c_int32, _P, _P, _S, _P]
 _lib.mla_attend_order_a.argtypes = [C.POINTER(Dims), _P, _P, _P, C.POINTER(CacheDesc), _P, C.c_int32, C.c_int32, _P,
                                     _P, _S, _P]
+_lib.mla_batch_plan.argtypes = [C.POINTER(CacheDesc), _P, _P, _P, C.c_int32, _P, C.c_int32, _P, C.c_int32, C.c_int32,
+                                _P, _P, _P, _P, _P, _P, _P]
+_lib.mla_cache_write.argtypes = [C.POINTER(Dims), _P, _P, C.c_int32, C.POINTER(CacheDesc), _P]
+_lib.mla_prefix_expand.argtypes = [C.POINTER(Dims), C.POINTER(CacheDesc), C.c_int32, C.c_int32, _P, _P, _P, _P, _P, _P]
+_lib.mla_decode_shared.argtypes = [C.POINTER(Dims), _P, _P, _P, _P, C.c_int32, C.POINTER(CacheDesc), _P, C.c_int32,
+                                   C.c_int32, _P, _P, _P, _P, _P, _S, _P]
 _lib.mla_workspace_size.argtypes = [C.POINTER(Dims), C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_int32]
 _lib.mla_workspace_size.restype = C.c_size_t
 _lib.mla_get_device_error.argtypes = [_P]
@@ -70,7 +76,8 @@ _lib.mla_kernel_launches.restype = C.c_uint64
 for _f in ("mla_cache_append", "mla_absorb_q", "mla_decode", "mla_decode_noalloc", "mla_out_proj", "mla_o_proj",
            "mla_get_device_error", "mla_set_launch_overlap", "mla_get_launch_overlap", "mla_absorb_wo",
            "mla_o_proj_latent", "mla_absorb_merge", "mla_absorb_q_merged", "mla_front_end", "mla_selftest_timeout",
-           "mla_query_heads", "mla_attend_order_a"):
+           "mla_query_heads", "mla_attend_order_a", "mla_batch_plan", "mla_cache_write", "mla_prefix_expand",
+           "mla_decode_shared"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -242,6 +249,99 @@ def mla_attend_order_a(p: Dims, qa, W_UK, W_UV, cache: Cache, seq_lens, n_q, o, 
     ws, nbytes = _ws(p, OP_ATTEND_A, B, n_q, ws, cache_rows(cache))
     _check(_lib.mla_attend_order_a(C.byref(p), _ptr(qa), _ptr(W_UK), _ptr(W_UV), C.byref(cache.desc), _ptr(seq_lens),
                                    B, n_q, _ptr(o), _ptr(ws), nbytes, _stream(stream)), "mla_attend_order_a")
+
+
+def _take(t, dtype, n, dev, what):
+    """A dense tensor of this type and element count on the device of the call
+    (these calls take their sizes from the tensors, so a wrong one must not
+    reach a kernel)."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of {n} elements on cuda:{dev} is needed, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _call_device(stream):
+    return torch.cuda.current_device() if stream is None else stream.device_index
+
+
+def _storage(p: Dims):
+    return torch.bfloat16 if p.dtype == MLA_BF16 else torch.float32
+
+
+def _take_cache(p: Dims, cache: Cache, dev, what):
+    data, table = cache.data, cache.block_table
+    if data.get_device() != dev or data.dtype is not _storage(p) or data.shape[-1] != p.d_c + p.d_r:
+        raise ValueError(f"{what}: a cache of {_storage(p)} rows of {p.d_c + p.d_r} on cuda:{dev} is needed, got "
+                         f"{data.dtype} {tuple(data.shape)} on {data.device}")
+    if table is not None and table.get_device() != dev:
+        raise ValueError(f"{what}: the block table is on {table.device}, the call on cuda:{dev}")
+    return C.byref(cache.desc)
+
+
+def mla_batch_plan(cache: Cache, ctx_lens, new_lens, free_blocks, seq_lens, row_start, seq_idx, positions, slots, used,
+                   shared_blocks=None, stream=None):
+    """Block tables and slot map of a step, from the requests' lengths: updates
+    cache.block_table in place and fills seq_lens [B], row_start [B + 1],
+    seq_idx, positions [T] (int32), slots [T] (int64) and used [1]. new_lens may
+    be None (one new token each)."""
+    table = cache.block_table
+    if table is None:
+        raise ValueError("mla_batch_plan: the cache must be paged")
+    dev, i32 = _call_device(stream), torch.int32
+    B, T, F = ctx_lens.numel(), seq_idx.numel(), free_blocks.numel()
+    S = 0 if shared_blocks is None else shared_blocks.numel()
+    if table.get_device() != dev:
+        raise ValueError(f"mla_batch_plan: the block table is on {table.device}, the call on cuda:{dev}")
+    _check(_lib.mla_batch_plan(
+        C.byref(cache.desc), table.data_ptr(), _take(ctx_lens, i32, B, dev, "ctx_lens"),
+        None if new_lens is None else _take(new_lens, i32, B, dev, "new_lens"), B,
+        _take(free_blocks, i32, F, dev, "free_blocks"), F,
+        None if shared_blocks is None else _take(shared_blocks, i32, S, dev, "shared_blocks"), S, T,
+        _take(seq_lens, i32, B, dev, "seq_lens"), _take(row_start, i32, B + 1, dev, "row_start"),
+        _take(seq_idx, i32, T, dev, "seq_idx"), _take(positions, i32, T, dev, "positions"),
+        _take(slots, torch.int64, T, dev, "slots"), _take(used, i32, 1, dev, "used"), _stream(stream)), "mla_batch_plan")
+
+
+def mla_cache_write(p: Dims, rows, slots, cache: Cache, stream=None):
+    """cache row slots[t] = rows[t] ([c_KV | k_R]); a negative slot is padding."""
+    dev, T = _call_device(stream), slots.numel()
+    desc = _take_cache(p, cache, dev, "mla_cache_write")
+    _check(_lib.mla_cache_write(C.byref(p), _take(rows, _storage(p), T * (p.d_c + p.d_r), dev, "rows"),
+                                _take(slots, torch.int64, T, dev, "slots"), T, desc, _stream(stream)),
+           "mla_cache_write")
+
+
+def mla_prefix_expand(p: Dims, cache: Cache, seq, W_UK, W_UV, kc, v, kr, stream=None):
+    """The first kr.shape[0] positions of cached sequence seq as per-head keys
+    and values: kc, v [n_h][P][d_h], kr [P][d_r] (outputs)."""
+    dev, dt, P, HD = _call_device(stream), _storage(p), kr.shape[0], p.n_h * p.d_h
+    desc = _take_cache(p, cache, dev, "mla_prefix_expand")
+    _check(_lib.mla_prefix_expand(C.byref(p), desc, int(seq), P, _take(W_UK, dt, HD * p.d_c, dev, "W_UK"),
+                                  _take(W_UV, dt, HD * p.d_c, dev, "W_UV"), _take(kc, dt, HD * P, dev, "kc"),
+                                  _take(v, dt, HD * P, dev, "v"), _take(kr, dt, P * p.d_r, dev, "kr"),
+                                  _stream(stream)), "mla_prefix_expand")
+
+
+def mla_decode_shared(p: Dims, qa, kc, v, kr, cache: Cache, seq_lens, n_q, W_UK, W_UV, o, lse=None, ws=None,
+                      stream=None):
+    """Decode of a batch whose sequences share the expanded prefix (kc, v
+    [n_h][P][d_h], kr [P][d_r] from mla_prefix_expand): qa [T][n_h][d_h + d_r]
+    from mla_query_heads, o [T][n_h * d_h]."""
+    dev, dt, P, HD = _call_device(stream), _storage(p), kr.shape[0], p.n_h * p.d_h
+    B = seq_lens.numel()
+    T = B * n_q
+    desc = _take_cache(p, cache, dev, "mla_decode_shared")
+    args = (_take(qa, dt, T * p.n_h * (p.d_h + p.d_r), dev, "qa"), _take(kc, dt, HD * P, dev, "kc"),
+            _take(v, dt, HD * P, dev, "v"), _take(kr, dt, P * p.d_r, dev, "kr"), P, desc,
+            _take(seq_lens, torch.int32, B, dev, "seq_lens"), B, n_q, _take(W_UK, dt, HD * p.d_c, dev, "W_UK"),
+            _take(W_UV, dt, HD * p.d_c, dev, "W_UV"), _take(o, dt, T * HD, dev, "o"),
+            None if lse is None else _take(lse, torch.float32, T * p.n_h, dev, "lse"))
+    if ws is None:
+        ws = torch.empty(workspace_size(p, OP_DECODE_SHARED, B, n_q, P), dtype=torch.uint8, device=qa.device)
+    nbytes = ws.numel() * ws.element_size()
+    _check(_lib.mla_decode_shared(C.byref(p), *args, _take(ws, ws.dtype, ws.numel(), dev, "ws"), nbytes,
+                                  _stream(stream)), "mla_decode_shared")
 
 
 def mla_selftest_timeout(wait_ns: int, scratch, stream=None):
