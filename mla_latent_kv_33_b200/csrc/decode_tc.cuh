@@ -621,7 +621,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == WARP_MMA) {
     // ------------------------------------------------------------ MMA issuer
-    if (rank == 0 && lane == 0) {
+    // (the whole warp walks the items; one elected lane issues)
+    if (warp_uniform(rank) == 0) {
+      const uint32_t tm = warp_uniform(tmem);
       PieceIter<kGrouped, kSkip> it = it0;
       Piece pc{};
       int gi = 0, nbig = 0, nsmall = 0, gz = 0, npc = 0, empty_bar = 0;
@@ -637,45 +639,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
           use = nsmall++;
         }
         empty_bar = BAR_BIG_EMPTY + slot;  // (small items are released by S_FULL)
-        if (!mbar_wait(bar(big ? BAR_BIG_FULL + slot : BAR_SMALL_FULL), use & 1, abort_flag)) return 0;
+        if (!mbar_wait_warp(bar(big ? BAR_BIG_FULL + slot : BAR_SMALL_FULL), use & 1, abort_flag)) return 0;
         tc_fence_after();
         return sbase + (big ? OFF_BIG + slot * BIG : OFF_SMALL);
       };
-      auto release = [&]() { tc_commit_pair(bar(empty_bar), 0x3); };
+      auto release = [&]() { tc_commit_pair(bar(empty_bar), 0x3); };  // by the elected lane
       // PV of global tile gt (tile ti of the current piece): A = P in tensor
       // memory; K step m of value item (vp, j) takes 8 tokens of block vp and 8
       // of block vp + 2 (one B descriptor over both halves of the item)
       auto issue_pv = [&](int gt, int ti, bool first) -> bool {
         const int zc = partial_chunk(pc.vis, ti);
-        const uint32_t p_col = tmem + S_COL + 128 * (gt & 1);
+        const uint32_t p_col = tm + S_COL + 128 * (gt & 1);
         for (int vp = 0; vp < 2; ++vp)
           for (int j = 0; j < 2; ++j) {
             const uint32_t vb = take(true);
             if (vb == 0) return false;
             if (vp == 0 && j == 0) {
-              if (!mbar_wait(bar(BAR_P_FULL), gt & 1, abort_flag)) return false;
-              if (first && npc > 0 && !mbar_wait(bar(BAR_O_FREE), (npc - 1) & 1, abort_flag)) return false;
+              if (!mbar_wait_warp(bar(BAR_P_FULL), gt & 1, abort_flag)) return false;
+              if (first && npc > 0 && !mbar_wait_warp(bar(BAR_O_FREE), (npc - 1) & 1, abort_flag)) return false;
               tc_fence_after();
             }
             if (zc >= 0 && vp == (zc & 1)) {  // both CTAs zero the rows past the end first
-              mbar_arrive(bar(BAR_V_LANDED));
-              mbar_arrive_cluster(mapa_shared(bar(BAR_V_LANDED), 1));
-              if (!mbar_wait(bar(BAR_ZERO_DONE), gz & 1, abort_flag)) return false;
+              if (lane == 0) {
+                mbar_arrive(bar(BAR_V_LANDED));
+                mbar_arrive_cluster(mapa_shared(bar(BAR_V_LANDED), 1));
+              }
+              if (!mbar_wait_warp(bar(BAR_ZERO_DONE), gz & 1, abort_flag)) return false;
               ++gz;
               tc_fence_after();
             }
             const uint64_t vd = sdesc_sw128(vb, ATOM, HALF);  // K step m: + 1024 bytes
+            if (elect_one()) {
 #pragma unroll
-            for (int m = 0; m < 8; ++m)
-              tc_mma_ts<2>(tmem + 128 * j, p_col + 8 * (8 * vp + m), sdesc_advance(vd, m * 1024), IDESC_PV,
-                           (first && vp == 0 && m == 0) ? 0u : 1u);
-            release();
+              for (int m = 0; m < 8; ++m)
+                tc_mma_ts<2>(tm + 128 * j, p_col + 8 * (8 * vp + m), sdesc_advance(vd, m * 1024), IDESC_PV,
+                             (first && vp == 0 && m == 0) ? 0u : 1u);
+              release();
+              if (vp == 1 && j == 1) tc_commit_pair(bar(BAR_O_FULL), 0x3);
+            }
+            __syncwarp();
           }
-        tc_commit_pair(bar(BAR_O_FULL), 0x3);
         return true;
       };
       while (ok && it.next(p, pc)) {
-        if (!mbar_wait(bar(BAR_Q_FULL), npc & 1, abort_flag)) break;
+        if (!mbar_wait_warp(bar(BAR_Q_FULL), npc & 1, abort_flag)) break;
         const int n = pc.t_end - pc.t_begin;
         for (int i = 0; i < n && ok; ++i, ++gi) {
           const int b = gi & 1;  // S(gi) goes over P(gi - 2), read by PV(gi - 2), issued before it
@@ -687,19 +694,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
             // their start address (+32 bytes per K step, + a chunk per c)
             const uint64_t qd = sdesc_sw128(sbase + OFF_Q + 2 * q * CHUNK_Q, 16, 1024);
             const uint64_t kd = sdesc_sw128(kbuf, 16, 1024);
+            if (elect_one()) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (!big && c == 1) break;
+              for (int c = 0; c < 2; ++c) {
+                if (!big && c == 1) break;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma<2>(tmem + S_COL + 128 * b, sdesc_advance(qd, c * CHUNK_Q + kk * 32),
-                          sdesc_advance(kd, c * CHUNK_K + kk * 32), IDESC_S, (q > 0 || c > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma<2>(tm + S_COL + 128 * b, sdesc_advance(qd, c * CHUNK_Q + kk * 32),
+                            sdesc_advance(kd, c * CHUNK_K + kk * 32), IDESC_S, (q > 0 || c > 0 || kk > 0) ? 1u : 0u);
+              }
+              if (big) {
+                release();
+              } else {  // the small item, the last one, is released by the S_FULL commit
+                tc_commit_pair(bar(BAR_S_FULL + b), 0x3);
+                if (i == n - 1) tc_commit_pair(bar(BAR_Q_EMPTY), 0x3);
+              }
             }
-            if (big) release();  // the small item is released by the S_FULL commit below
+            __syncwarp();
           }
           if (!ok) break;
-          tc_commit_pair(bar(BAR_S_FULL + b), 0x3);
-          if (i == n - 1) tc_commit_pair(bar(BAR_Q_EMPTY), 0x3);
           if (i > 0 && !issue_pv(gi - 1, pc.t_begin + i - 1, i == 1)) { ok = false; break; }
         }
         if (!ok) break;

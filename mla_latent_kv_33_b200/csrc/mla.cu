@@ -42,11 +42,11 @@ std::atomic<uint64_t> g_launches{0};
 std::atomic<int> g_overlap{0};
 
 // Launch of a tensor-core kernel: plain, or with programmatic stream
-// serialization while launch overlap is on (the kernels wait for the grid
-// ahead of them with griddepcontrol.wait before touching its outputs).
+// serialization (the kernels wait for the grid ahead of them with
+// griddepcontrol.wait before touching its outputs).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_tc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                      Args &&...args) {
+cudaError_t launch_pdl(bool overlap, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                       Args &&...args) {
   g_launches.fetch_add(1, std::memory_order_relaxed);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -57,8 +57,17 @@ cudaError_t launch_tc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = g_overlap.load(std::memory_order_relaxed) ? 1 : 0;
+  cfg.numAttrs = overlap ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The first (or only) kernel of a call: overlapped with the work before the
+// call while launch overlap is on.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_tc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                      Args &&...args) {
+  return launch_pdl(g_overlap.load(std::memory_order_relaxed) != 0, kernel, grid, block, smem, st,
+                    std::forward<Args>(args)...);
 }
 
 mla_status fail(mla_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
@@ -91,7 +100,8 @@ mla_status launched(cudaError_t e, const char *what) {
 // shared memory limit is raised once per device (bit `device` of its mask).
 enum SmemKernel {
   SMEM_GEMM = 0, SMEM_ABSORB = 1, SMEM_DECODE = 2, SMEM_ATTEND_A = 3, SMEM_DECODE_NQ = 4, SMEM_GEMM_RES = 5,
-  SMEM_EXPAND = 6, SMEM_DECODE_SUFFIX = 7, SMEM_DECODE_SUFFIX_NQ = 8, SMEM_PREFIX = 9, SMEM_PLAN = 10, SMEM_KERNELS = 11
+  SMEM_EXPAND = 6, SMEM_DECODE_SUFFIX = 7, SMEM_DECODE_SUFFIX_NQ = 8, SMEM_PREFIX = 9, SMEM_PREFIX_PAIR = 10, SMEM_SHARED_OUT = 11,
+  SMEM_PLAN = 12, SMEM_KERNELS = 13
 };
 std::atomic<uint64_t> g_smem_raised[SMEM_KERNELS];
 
@@ -1085,8 +1095,10 @@ int decode_clusters(int sms) {
 }
 
 // skip > 0: attend to positions skip .. only (the suffix of a shared prefix).
+// chained: not the first launch of its call, so always overlapped with it.
 mla_status decode_tc(const mla_dims *d, const void *q, const mla_cache *c, const int32_t *seq_lens, int B, int n_q,
-                     void *o_lat, float *lse, int num_splits, void *ws, size_t ws_bytes, cudaStream_t st, int skip = 0) {
+                     void *o_lat, float *lse, int num_splits, void *ws, size_t ws_bytes, cudaStream_t st, int skip = 0,
+                     bool chained = false) {
   namespace D = mla::dec;
   const int BJ = B * n_q;
   if (BJ > D::MAX_UNITS) return fail(MLA_ERR_UNSUPPORTED, "tensor-core decode supports B*n_q <= %d", D::MAX_UNITS);
@@ -1156,11 +1168,12 @@ mla_status decode_tc(const mla_dims *d, const void *q, const mla_cache *c, const
   if ((s = raise_smem_limit(reinterpret_cast<const void *>(kernel), which, D::SMEM_BYTES,
                             "decode: set shared memory size")) != MLA_OK)
     return s;
-  if ((s = launched(launch_tc(kernel, dim3(2 * nclusters), dim3(D::NUM_THREADS), D::SMEM_BYTES, st, tm_q, tm_k, tm_v[0],
-                              tm_v[1], p),
+  const bool overlap = chained || g_overlap.load(std::memory_order_relaxed) != 0;
+  if ((s = launched(launch_pdl(overlap, kernel, dim3(2 * nclusters), dim3(D::NUM_THREADS), D::SMEM_BYTES, st, tm_q, tm_k,
+                               tm_v[0], tm_v[1], p),
                     "decode (tensor cores)")) != MLA_OK)
     return s;
-  return launched(launch_tc(D::k_combine, dim3(BJ * D::COMBINE_BLOCKS_PER_ROW), dim3(128), 0, st, p),
+  return launched(launch_pdl(overlap, D::k_combine, dim3(BJ * D::COMBINE_BLOCKS_PER_ROW), dim3(128), 0, st, p),
                   "decode combine");
 }
 
@@ -1211,12 +1224,12 @@ mla_status simt_prefix_expand(const mla_dims *d, const mla_cache *c, int seq, in
   return cuda_check("prefix expansion (CUDA cores)");
 }
 
-// Workspace of a shared-prefix decode: absorbed queries, the suffix's latent
-// readout, its lse and its W_UV readout, the prefix partials, and the suffix
-// decode's own workspace.
+// Workspace of a shared-prefix decode: absorbed queries and what their rounding
+// took off, the suffix's latent readout and lse, the prefix partials, and the
+// suffix decode's own workspace.
 struct SharedPlan {
-  int T, nt, units, ctas, part_rows;
-  size_t q, o_lat, lse_s, o_s, part_o, part_lse, dec, total;
+  int T, cg, nt, units, clusters, part_rows;  // cg: CTAs per cluster of the prefix attention
+  size_t q, q_lo, o_lat, lse_s, part_o, part_lse, dec, total;
 };
 
 SharedPlan shared_plan(const mla_dims *d, int B, int n_q, int64_t P) {
@@ -1225,10 +1238,15 @@ SharedPlan shared_plan(const mla_dims *d, int B, int n_q, int64_t P) {
   const size_t T = static_cast<size_t>(B) * n_q, H = d->n_h;
   const int sms = sm_count();
   w.T = B * n_q;
+  // one block of 128 rows: one CTA per range. More rows: pairs of CTAs that
+  // share every key tile.
+  w.cg = w.T > X::QROWS ? 2 : 1;
   w.nt = static_cast<int>((P + X::KTILE - 1) / X::KTILE);
-  w.units = (w.T + X::QROWS - 1) / X::QROWS * d->n_h;
-  w.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, static_cast<int64_t>(w.units) * w.nt)));
-  w.part_rows = std::min(w.T, static_cast<int>(X::QROWS));
+  w.units = (w.T + X::QROWS * w.cg - 1) / (X::QROWS * w.cg) * d->n_h;
+  // (k_shared_out joins at most three partials: a range holds more than half a unit's tiles)
+  const int room = std::min(w.cg == 2 ? decode_clusters(sms) : sms, w.units * 3 / 2);
+  w.clusters = static_cast<int>(std::min<int64_t>(room, static_cast<int64_t>(w.units) * (w.nt + X::ABS)));
+  w.part_rows = std::min(w.T, X::QROWS * w.cg);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -1236,10 +1254,10 @@ SharedPlan shared_plan(const mla_dims *d, int B, int n_q, int64_t P) {
     return o;
   };
   w.q = take(T * H * (d->d_c + d->d_r) * 2);
+  w.q_lo = take(T * H * d->d_c * 2);
   w.o_lat = take(T * H * d->d_c * 2);
   w.lse_s = take(T * H * sizeof(float));
-  w.o_s = take(T * H * d->d_h * 2);
-  const size_t slots = P > 0 ? static_cast<size_t>(w.units) + w.ctas : 0;
+  const size_t slots = P > 0 ? static_cast<size_t>(w.units) + (w.cg == 2 ? sms / 2 : sms) : 0;
   w.part_o = take(slots * w.part_rows * d->d_h * sizeof(float));
   w.part_lse = take(slots * w.part_rows * sizeof(float));
   w.dec = at;
@@ -1259,29 +1277,27 @@ mla_status tc_decode_shared(const mla_dims *d, const void *qa, const void *kc, c
     return fail(MLA_ERR_UNSUPPORTED, "decode_shared needs prefix_len to be a multiple of 64 on a paged cache");
   const SharedPlan w = shared_plan(d, B, n_q, P);
   uint8_t *w8 = static_cast<uint8_t *>(ws);
-  __nv_bfloat16 *q = reinterpret_cast<__nv_bfloat16 *>(w8 + w.q), *o_lat = reinterpret_cast<__nv_bfloat16 *>(w8 + w.o_lat),
-                *o_s = reinterpret_cast<__nv_bfloat16 *>(w8 + w.o_s);
+  __nv_bfloat16 *q = reinterpret_cast<__nv_bfloat16 *>(w8 + w.q), *q_lo = reinterpret_cast<__nv_bfloat16 *>(w8 + w.q_lo),
+                *o_lat = reinterpret_cast<__nv_bfloat16 *>(w8 + w.o_lat);
   float *lse_s = reinterpret_cast<float *>(w8 + w.lse_s);
-  const int T = w.T, HD = d->n_h * d->d_h, HQ = d->n_h * X::DQK;
+  const int T = w.T, HD = d->n_h * d->d_h;
+  const uint64_t H = d->n_h, uT = T, uP = P;
   mla_status s;
-  // prefix attention, and q_R into the absorbed queries
-  CUtensorMap tm_q, tm_kc, tm_kr, tm_v;
+  // prefix attention, and the absorbed queries [W_UK_h^T q_C,h | q_R,h]
+  CUtensorMap tm_q, tm_kc, tm_kr, tm_v, tm_uk;
   {
-    const uint64_t dims[3] = {static_cast<uint64_t>(X::DQK), static_cast<uint64_t>(d->n_h), static_cast<uint64_t>(T)};
-    const uint64_t str[2] = {X::DQK * 2ull, static_cast<uint64_t>(d->n_h) * X::DQK * 2};
+    const uint64_t dims[3] = {X::DQK, H, uT}, str[2] = {X::DQK * 2ull, H * X::DQK * 2};
     const uint32_t box[3] = {64, 1, X::QROWS};
     if ((s = make_tmap_nd(&tm_q, qa, 3, dims, str, box, "qa")) != MLA_OK) return s;
   }
-  tm_kc = tm_kr = tm_v = tm_q;  // P = 0: nothing is loaded
+  if ((s = make_tmap_bf16(&tm_uk, W_UK, d->d_c, HD, d->d_c * 2ull, 64, 128, "W_UK")) != MLA_OK) return s;
+  tm_kc = tm_kr = tm_v = tm_q;  // P = 0: nothing is loaded through these
   if (P > 0) {
-    for (int u = 0; u < 2; ++u) {
-      const uint64_t dims[3] = {static_cast<uint64_t>(d->d_h), static_cast<uint64_t>(P), static_cast<uint64_t>(d->n_h)};
-      const uint64_t str[2] = {d->d_h * 2ull, static_cast<uint64_t>(P) * d->d_h * 2};
-      const uint32_t box[3] = {64, X::KTILE, 1};
-      if ((s = make_tmap_nd(u == 0 ? &tm_kc : &tm_v, u == 0 ? kc : v, 3, dims, str, box, u == 0 ? "kc" : "v")) != MLA_OK)
-        return s;
-    }
-    if ((s = make_tmap_bf16(&tm_kr, kr, d->d_r, P, d->d_r * 2ull, 64, X::KTILE, "kr")) != MLA_OK) return s;
+    const uint64_t dims[3] = {X::DV, uP, H}, str[2] = {X::DV * 2ull, uP * X::DV * 2};
+    const uint32_t rows = X::KTILE / w.cg, box_k[3] = {64, rows, 1}, box_v[3] = {64, X::KTILE, 1};
+    if ((s = make_tmap_nd(&tm_kc, kc, 3, dims, str, box_k, "kc")) != MLA_OK) return s;
+    if ((s = make_tmap_nd(&tm_v, v, 3, dims, str, box_v, "v")) != MLA_OK) return s;
+    if ((s = make_tmap_bf16(&tm_kr, kr, d->d_r, P, d->d_r * 2ull, 64, rows, "kr")) != MLA_OK) return s;
   }
   X::Params xp{};
   xp.T = T;
@@ -1295,53 +1311,54 @@ mla_status tc_decode_shared(const mla_dims *d, const void *qa, const void *kc, c
   xp.part_lse = reinterpret_cast<float *>(w8 + w.part_lse);
   xp.qa = static_cast<const __nv_bfloat16 *>(qa);
   xp.q = q;
-  if ((s = raise_smem_limit(reinterpret_cast<const void *>(X::k_prefix_attend), SMEM_PREFIX, X::SMEM_BYTES,
-                            "prefix attention: set shared memory size")) != MLA_OK)
+  xp.q_lo = lse != nullptr ? q_lo : nullptr;
+  const auto kernel = w.cg == 2 ? X::k_prefix_attend<2> : X::k_prefix_attend<1>;
+  if ((s = raise_smem_limit(reinterpret_cast<const void *>(kernel), w.cg == 2 ? SMEM_PREFIX_PAIR : SMEM_PREFIX,
+                            X::SMEM_BYTES, "prefix attention: set shared memory size")) != MLA_OK)
     return s;
-  if ((s = launched(launch_tc(X::k_prefix_attend, dim3(w.ctas), dim3(X::NUM_THREADS), X::SMEM_BYTES, st, tm_q, tm_kc,
-                              tm_kr, tm_v, xp),
+  if ((s = launched(launch_tc(kernel, dim3(w.cg * w.clusters), dim3(X::NUM_THREADS), X::SMEM_BYTES, st, tm_q, tm_kc,
+                              tm_kr, tm_v, tm_uk, xp),
                     "prefix attention (tensor cores)")) != MLA_OK)
     return s;
-  // q_lat,h = W_UK_h^T q_C,h, straight from qa (the q_C columns of head h)
+  // the suffix, absorbed; this and the readout are overlapped with the launch
+  // before them whatever the switch says: what they touch before they wait for
+  // it (W_UV) was written before the call's first kernel started
+  if ((s = decode_tc(d, q, c, seq_lens, B, n_q, o_lat, lse_s, 0, w8 + w.dec, ws_bytes - w.dec, st, P, true)) != MLA_OK)
+    return s;
+  // its W_UV readout, joined with the prefix
+  CUtensorMap tm_o, tm_uv, tm_lo;
   {
-    const int64_t Dq = d->d_c + d->d_r;
-    const GemmShape g = gemm_shape(d->d_c, T, d->d_h, d->n_h, false);
-    CUtensorMap ta, tb;
-    if ((s = make_tmap_bf16(&ta, W_UK, d->d_c, HD, d->d_c * 2ull, 64, 64, "W_UK")) != MLA_OK) return s;
-    if ((s = make_tmap_bf16(&tb, qa, HQ, T, HQ * 2ull, 64, g.n_tile, "qa (q_C)")) != MLA_OK) return s;
-    G::Params p{};
-    p.epi = G::EPI_BF16;
-    p.dst = q;
-    p.e_bs = Dq;
-    p.e_ns = d->n_h * Dq;
-    GemmOperands op = operands(ta, tb);
-    op.a_mn_major = true;
-    op.a_batch_rows = d->d_h;
-    op.b_batch_cols = X::DQK;
-    if ((s = launch_gemm(op, g, T, p, st)) != MLA_OK) return s;
+    const uint64_t dims[3] = {X::DC, H, uT}, str[2] = {X::DC * 2ull, H * X::DC * 2};
+    const uint32_t box[3] = {64, 1, X::QROWS};
+    if ((s = make_tmap_nd(&tm_o, o_lat, 3, dims, str, box, "o_lat")) != MLA_OK) return s;
+    if ((s = make_tmap_nd(&tm_lo, q_lo, 3, dims, str, box, "q_lo")) != MLA_OK) return s;
   }
-  // the suffix, absorbed, and its W_UV readout
-  if ((s = decode_tc(d, q, c, seq_lens, B, n_q, o_lat, lse_s, 0, w8 + w.dec, ws_bytes - w.dec, st, P)) != MLA_OK) return s;
-  if ((s = tc_out_proj(d, o_lat, W_UV, T, o_s, nullptr, st)) != MLA_OK) return s;
-  X::MergeParams mp{};
-  mp.T = T;
-  mp.n_q = n_q;
-  mp.P = P;
-  mp.nt = w.nt;
-  mp.units = w.units;
-  mp.part_rows = w.part_rows;
-  mp.ctas = w.ctas;
-  mp.capacity = cache_capacity(c);
-  mp.seq_lens = seq_lens;
-  mp.part_o = xp.part_o;
-  mp.part_lse = xp.part_lse;
-  mp.o_s = o_s;
-  mp.lse_s = lse_s;
-  mp.o = static_cast<__nv_bfloat16 *>(o);
-  mp.lse = lse;
-  const int64_t warps = static_cast<int64_t>(T) * d->n_h;
-  return launched(launch_tc(X::k_merge_shared, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, st, mp),
-                  "shared-prefix merge");
+  if ((s = make_tmap_bf16(&tm_uv, W_UV, d->d_c, HD, d->d_c * 2ull, 64, 128, "W_UV")) != MLA_OK) return s;
+  X::so::Params op{};
+  op.T = T;
+  op.n_q = n_q;
+  op.P = P;
+  op.nt = w.nt;
+  op.units = w.units;
+  op.part_rows = w.part_rows;
+  op.clusters = w.clusters;
+  op.group = w.cg;
+  op.capacity = cache_capacity(c);
+  op.scale = xp.scale;
+  op.seq_lens = seq_lens;
+  op.part_o = xp.part_o;
+  op.part_lse = xp.part_lse;
+  op.lse_s = lse_s;
+  op.o = static_cast<__nv_bfloat16 *>(o);
+  op.lse = lse;
+  const int ctas = (T + X::QROWS - 1) / X::QROWS * d->n_h;
+  op.stages = X::so::stages(ctas, sm_count());
+  if ((s = raise_smem_limit(reinterpret_cast<const void *>(X::k_shared_out), SMEM_SHARED_OUT,
+                            X::so::smem_bytes(X::so::MAX_STAGES), "suffix readout: set shared memory size")) != MLA_OK)
+    return s;
+  return launched(launch_pdl(true, X::k_shared_out, dim3(ctas), dim3(X::so::NUM_THREADS), X::so::smem_bytes(op.stages),
+                             st, tm_o, tm_uv, tm_lo, op),
+                  "suffix readout and join (tensor cores)");
 }
 
 template <typename T>

@@ -9,7 +9,8 @@ u times the value; the roundings that are summed over many terms (P, the latent
 readout, the absorbed query) are independent, each with a standard deviation of
 at most u / sqrt(3) of its value, and are bounded by six standard deviations of
 their sum, formed per output element in 64 bits (6 sigma: 2e-9 per element).
-fp32 sums and exponentials add at most 2e-5."""
+The lse is fp32: the first order of the absorbed query's rounding is corrected,
+its second order remains. fp32 sums and exponentials add at most 2e-5."""
 import math
 
 import numpy as np
@@ -130,7 +131,9 @@ def reference(pr, scale):
                 # the absorbed query: ds_i = scale sum_j dq_j c_ij moves o by sum_i w_i ds_i (v_i - o)
                 cov = torch.einsum("hn,nc,hnd->hcd", ws, c[:n], vs) - lat[:, :, None] * o[t][:, None]
                 tol[t] += six * scale * torch.einsum("hc,hcd->hd", q_lat ** 2, cov ** 2).sqrt()
-                ltol[t] += six * scale * ((q_lat * lat) ** 2).sum(dim=1).sqrt()
+                # lse: the first order of ds is added back (with the rounded latent readout); its square is left
+                ds = six * scale * ((q_lat ** 2) @ (c[:n] ** 2).t()).amax(dim=1).sqrt()
+                ltol[t] += ds ** 2 / 2 + u * ds
     return o.view(pr.T, -1), lse, tol.view(pr.T, -1), ltol
 
 
