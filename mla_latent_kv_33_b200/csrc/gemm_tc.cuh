@@ -681,33 +681,39 @@ __global__ void __launch_bounds__(rs::NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
-    if (rank == 0 && lane == 0) {
+    // (the whole warp walks the units; one elected lane issues)
+    if (warp_uniform(rank) == 0) {
       constexpr uint32_t idesc = idesc_bf16(2 * BM, rs::NT, false, false);
+      const uint32_t tm = warp_uniform(tmem);
       const uint64_t a0 = sdesc_sw128(sbase, 16, 1024);
       int na = 0, g = 0, lt = 0;
       bool ok = true;
       for (int u = u0; u < u1 && ok; ++u, ++lt) {
         if (pair_start(u)) {
-          if (!(ok = mbar_wait(bar(rs::BAR_A_FULL), na & 1, abort_flag))) break;
+          if (!(ok = mbar_wait_warp(bar(rs::BAR_A_FULL), na & 1, abort_flag))) break;
           ++na;
         }
         const int buf = lt & 1;
-        if (lt >= 2 && !(ok = mbar_wait(bar(rs::BAR_ACC_EMPTY + buf), ((lt >> 1) - 1) & 1, abort_flag))) break;
+        if (lt >= 2 && !(ok = mbar_wait_warp(bar(rs::BAR_ACC_EMPTY + buf), ((lt >> 1) - 1) & 1, abort_flag))) break;
         tc_fence_after();
         for (int kb = 0; kb < p.kblk; ++kb, ++g) {
           const int s = g % rs::STAGES;
-          if (!(ok = mbar_wait(bar(rs::BAR_B_FULL + s), (g / rs::STAGES) & 1, abort_flag))) break;
+          if (!(ok = mbar_wait_warp(bar(rs::BAR_B_FULL + s), (g / rs::STAGES) & 1, abort_flag))) break;
           tc_fence_after();
           const uint64_t bd = sdesc_sw128(sbase + rs::OFF_B + s * rs::B_STAGE, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma<2>(tmem + 256 * buf, sdesc_advance(a0, kb * rs::A_BLK + kk * 32), sdesc_advance(bd, kk * 32), idesc,
-                      (kb > 0 || kk > 0) ? 1u : 0u);
-          tc_commit_pair(bar(rs::BAR_B_EMPTY + s), 0x3);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              tc_mma<2>(tm + 256 * buf, sdesc_advance(a0, kb * rs::A_BLK + kk * 32), sdesc_advance(bd, kk * 32), idesc,
+                        (kb > 0 || kk > 0) ? 1u : 0u);
+            tc_commit_pair(bar(rs::BAR_B_EMPTY + s), 0x3);
+            if (kb + 1 == p.kblk) {
+              tc_commit_pair(bar(rs::BAR_ACC_FULL + buf), 0x3);
+              if (u + 1 == u1 || (u + 1) % p.n_tiles == 0) tc_commit_pair(bar(rs::BAR_A_EMPTY), 0x3);
+            }
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        tc_commit_pair(bar(rs::BAR_ACC_FULL + buf), 0x3);
-        if (u + 1 == u1 || (u + 1) % p.n_tiles == 0) tc_commit_pair(bar(rs::BAR_A_EMPTY), 0x3);
       }
     }
   } else if ((warp >= 2 && warp < 6) || warp >= 8) {

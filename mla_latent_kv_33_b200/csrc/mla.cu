@@ -1802,13 +1802,13 @@ mla_status mla_batch_plan(const mla_cache *c, int32_t *block_table, const int32_
   p.block_size = c->block_size;
   p.max_blocks = c->max_blocks_per_seq;
   mla_status s = raise_smem_limit(reinterpret_cast<const void *>(N::k_batch_plan), SMEM_PLAN,
-                                  2 * N::MAX_REQUESTS * static_cast<int>(sizeof(int32_t)),
+                                  3 * N::MAX_REQUESTS * static_cast<int>(sizeof(int32_t)),
                                   "batch plan: set shared memory size");
   if (s != MLA_OK) return s;
   const int64_t items = std::max<int64_t>(T, static_cast<int64_t>(B) * num_shared);
   const int64_t blocks = std::min<int64_t>((items + 2 * N::PLAN_THREADS - 1) / (2 * N::PLAN_THREADS), sm_count());
   return launched(launch_tc(N::k_batch_plan, dim3(static_cast<unsigned>(blocks)), dim3(N::PLAN_THREADS),
-                            2 * sizeof(int32_t) * B, static_cast<cudaStream_t>(stream), p),
+                            3 * sizeof(int32_t) * B, static_cast<cudaStream_t>(stream), p),
                   "batch plan");
 }
 

