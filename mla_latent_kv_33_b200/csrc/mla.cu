@@ -118,6 +118,8 @@ mla_status raise_smem_limit(const void *kernel, SmemKernel which, int bytes, con
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 size_t elem_size(const mla_dims *d) { return d->dtype == MLA_BF16 ? 2 : 4; }
 
 float softmax_scale(const mla_dims *d) {
@@ -927,6 +929,7 @@ mla_status tc_attend_a(const mla_dims *d, const void *qa, const void *W_UK, cons
     rp.kblk = d->d_c / G::BK;
     rp.out0 = kc;
     rp.out1 = vv;
+    rp.wide = aligned32(kc) && aligned32(vv);
     const int grid = 2 * std::max(1, std::min(sm_count() / 2, (rp.batches / 2) * rp.n_tiles));  // clusters of 2
     if ((s = raise_smem_limit(reinterpret_cast<const void *>(G::k_gemm_resident<false>), SMEM_GEMM_RES, G::rs::SMEM_BYTES,
                               "decompression: set shared memory size")) != MLA_OK)
@@ -1201,6 +1204,7 @@ mla_status tc_prefix_expand(const mla_dims *d, const mla_cache *c, int seq, int 
   rp.kblk = d->d_c / G::BK;
   rp.out0 = static_cast<__nv_bfloat16 *>(kc);
   rp.out1 = static_cast<__nv_bfloat16 *>(v);
+  rp.wide = aligned32(kc) && aligned32(v);
   rp.cache = view_of(c);
   rp.seq = seq;
   rp.oob_row = static_cast<int>(R);

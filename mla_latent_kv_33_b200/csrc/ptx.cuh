@@ -175,6 +175,13 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   return r;
 }
 
+// 32 bytes (a whole sector) in one store; dst is 32-byte aligned.
+__device__ __forceinline__ void st_global_32(void *dst, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Registers of the calling warpgroup (all four of its warps call it): give back
 // down to N, or take up to N of what the block was launched with.
 template <int N>
