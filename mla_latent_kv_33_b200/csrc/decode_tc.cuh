@@ -776,6 +776,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
         const float mo = m_ref * c2;
         float ps = 0.f;
         uint4 *xb = reinterpret_cast<uint4 *>(smem + OFF_XBUF);
+        const int xsw = (L >> 1) & 3;  // word u of row L sits at u ^ xsw: no bank conflicts either way
 #pragma unroll 1
         for (int q4 = 0; q4 < 4; ++q4) {
           uint32_t sr[32];
@@ -791,12 +792,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
             pk[c] = pack_bf16x2(p0, p1);
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) xb[L * 4 + u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+          for (int u = 0; u < 4; ++u) xb[L * 4 + (u ^ xsw)] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
           named_bar_sync(1, 128);
           uint32_t pw[32];
 #pragma unroll
           for (int gg = 0; gg < 4; ++gg) {
-            const uint4 o = xb[(L ^ 64) * 4 + gg];
+            const uint4 o = xb[(L ^ 64) * 4 + (gg ^ xsw)];
             const uint32_t mine[4] = {pk[4 * gg], pk[4 * gg + 1], pk[4 * gg + 2], pk[4 * gg + 3]};
             const uint32_t theirs[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
