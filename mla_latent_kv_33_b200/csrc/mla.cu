@@ -101,7 +101,7 @@ mla_status launched(cudaError_t e, const char *what) {
 enum SmemKernel {
   SMEM_GEMM = 0, SMEM_ABSORB = 1, SMEM_DECODE = 2, SMEM_ATTEND_A = 3, SMEM_DECODE_NQ = 4, SMEM_GEMM_RES = 5,
   SMEM_EXPAND = 6, SMEM_DECODE_SUFFIX = 7, SMEM_DECODE_SUFFIX_NQ = 8, SMEM_PREFIX = 9, SMEM_PREFIX_PAIR = 10, SMEM_SHARED_OUT = 11,
-  SMEM_PLAN = 12, SMEM_KERNELS = 13
+  SMEM_SHARED_OUT_TWO = 12, SMEM_PLAN = 13, SMEM_KERNELS = 14
 };
 std::atomic<uint64_t> g_smem_raised[SMEM_KERNELS];
 
@@ -1269,10 +1269,6 @@ SharedPlan shared_plan(const mla_dims *d, int B, int n_q, int64_t P) {
   return w;
 }
 
-size_t simt_shared_ws(const mla_dims *d, int T) {  // q_lat, fp32
-  return sizeof(float) * static_cast<size_t>(T) * d->n_h * d->d_c;
-}
-
 mla_status tc_decode_shared(const mla_dims *d, const void *qa, const void *kc, const void *v, const void *kr, int P,
                             const mla_cache *c, const int32_t *seq_lens, int B, int n_q, const void *W_UK,
                             const void *W_UV, void *o, float *lse, void *ws, size_t ws_bytes, cudaStream_t st) {
@@ -1356,27 +1352,24 @@ mla_status tc_decode_shared(const mla_dims *d, const void *qa, const void *kc, c
   op.o = static_cast<__nv_bfloat16 *>(o);
   op.lse = lse;
   const int ctas = (T + X::QROWS - 1) / X::QROWS * d->n_h;
-  op.stages = X::so::stages(ctas, sm_count());
-  if ((s = raise_smem_limit(reinterpret_cast<const void *>(X::k_shared_out), SMEM_SHARED_OUT,
-                            X::so::smem_bytes(X::so::MAX_STAGES), "suffix readout: set shared memory size")) != MLA_OK)
+  const bool two = ctas > sm_count();  // CTAs per SM
+  op.stages = two ? 2 : X::so::MAX_STAGES;
+  const auto out_kernel = two ? X::k_shared_out<2> : X::k_shared_out<1>;
+  if ((s = raise_smem_limit(reinterpret_cast<const void *>(out_kernel), two ? SMEM_SHARED_OUT_TWO : SMEM_SHARED_OUT,
+                            X::so::smem_bytes(op.stages), "suffix readout: set shared memory size")) != MLA_OK)
     return s;
-  return launched(launch_pdl(true, X::k_shared_out, dim3(ctas), dim3(X::so::NUM_THREADS), X::so::smem_bytes(op.stages),
-                             st, tm_o, tm_uv, tm_lo, op),
+  return launched(launch_pdl(true, out_kernel, dim3(ctas), dim3(X::so::NUM_THREADS), X::so::smem_bytes(op.stages), st,
+                             tm_o, tm_uv, tm_lo, op),
                   "suffix readout and join (tensor cores)");
 }
 
 template <typename T>
 mla_status simt_decode_shared(const mla_dims *d, const void *qa, const void *kc, const void *v, const void *kr, int P,
                               const mla_cache *c, const int32_t *seq_lens, int B, int n_q, const void *W_UK,
-                              const void *W_UV, void *o, float *lse, void *ws, cudaStream_t st) {
-  const int64_t HQ = static_cast<int64_t>(d->n_h) * (d->d_h + d->d_r), HC = static_cast<int64_t>(d->n_h) * d->d_c;
-  float *q_lat = static_cast<float *>(ws);  // [T][n_h][d_c]
-  // q_lat,h[j] = sum_i W_UK[h*d_h + i][j] q_C,h[i]: batch = head, W(h, n=j, k=i)
-  launch_linear<T>(static_cast<const T *>(W_UK), static_cast<int64_t>(d->d_h) * d->d_c, 1, d->d_c, qa, false,
-                   d->d_h + d->d_r, HQ, q_lat, d->d_c, HC, d->d_c, d->d_h, B * n_q, d->n_h, st);
+                              const void *W_UV, void *o, float *lse, cudaStream_t st) {
   const size_t smem = sizeof(float) * (d->d_h + d->d_r + 2 * static_cast<size_t>(d->d_c));
-  MLA_LAUNCH(mla::k_simt_shared<T><<<B * n_q * d->n_h, 256, smem, st>>>(
-      static_cast<const T *>(qa), q_lat, static_cast<const T *>(kc), static_cast<const T *>(v),
+  MLA_LAUNCH(mla::k_simt_shared<T><<<B * n_q * d->n_h, 1024, smem, st>>>(
+      static_cast<const T *>(qa), static_cast<const T *>(W_UK), static_cast<const T *>(kc), static_cast<const T *>(v),
       static_cast<const T *>(kr), P, view_of(c), seq_lens, n_q, d->n_h, d->d_h, d->d_c, d->d_r, softmax_scale(d),
       static_cast<const T *>(W_UV), static_cast<T *>(o), lse));
   return cuda_check("shared-prefix decode (CUDA cores)");
@@ -1517,7 +1510,7 @@ size_t mla_workspace_size(const mla_dims *d, int32_t op, int32_t rows, int32_t n
     case MLA_OP_DECODE_SHARED: {
       const int64_t T = static_cast<int64_t>(rows) * (n_q < 1 ? 1 : n_q);
       if (T > mla::dec::MAX_UNITS || max_seq_len < 0 || max_seq_len > INT32_MAX) return 0;
-      return tc ? shared_plan(d, rows, n_q < 1 ? 1 : n_q, max_seq_len).total : simt_shared_ws(d, static_cast<int>(T));
+      return tc ? shared_plan(d, rows, n_q < 1 ? 1 : n_q, max_seq_len).total : 0;
     }
   }
   return 0;
@@ -1877,8 +1870,8 @@ mla_status mla_decode_shared(const mla_dims *d, const void *qa, const void *kc, 
   if (tc_geometry(d))
     return tc_decode_shared(d, qa, kc, v, kr, prefix_len, c, seq_lens, B, n_q, W_UK, W_UV, o, lse, ws, ws_bytes, st);
   if (d->dtype == MLA_BF16)
-    return simt_decode_shared<__nv_bfloat16>(d, qa, kc, v, kr, prefix_len, c, seq_lens, B, n_q, W_UK, W_UV, o, lse, ws, st);
-  return simt_decode_shared<float>(d, qa, kc, v, kr, prefix_len, c, seq_lens, B, n_q, W_UK, W_UV, o, lse, ws, st);
+    return simt_decode_shared<__nv_bfloat16>(d, qa, kc, v, kr, prefix_len, c, seq_lens, B, n_q, W_UK, W_UV, o, lse, st);
+  return simt_decode_shared<float>(d, qa, kc, v, kr, prefix_len, c, seq_lens, B, n_q, W_UK, W_UV, o, lse, st);
 }
 
 mla_status mla_selftest_timeout(uint64_t wait_ns, void *scratch, size_t scratch_bytes, void *stream) {

@@ -535,7 +535,6 @@ constexpr int MAX_PARTS = 3;
 constexpr int NUM_THREADS = 384, STAGE = 3 * CHUNK, BK = 64, KB = DC / BK;
 constexpr int PITCH = DV + 4;  // floats per row of the staged o_S: conflict-free for 16-byte words
 constexpr int MAX_STAGES = 4;
-inline int stages(int ctas, int sms) { return ctas > sms ? 2 : MAX_STAGES; }  // two CTAs per SM, or one
 constexpr int smem_bytes(int stages) { return stages * STAGE + 8 * (2 * MAX_STAGES + 1) + 16 + 3 * 128 * 4 + 1024; }
 static_assert(2 * STAGE >= QROWS * PITCH * 4, "o_S is staged over the pipeline's stages");
 static_assert(2 * smem_bytes(2) <= 232448 && smem_bytes(MAX_STAGES) <= 232448, "suffix readout shared memory budget");
@@ -551,9 +550,11 @@ struct Params {
 };
 }  // namespace so
 
-__global__ void __launch_bounds__(so::NUM_THREADS, 2)
+template <int CTAS>  // per SM (registers for 8 or 4 rows' loads in flight per warp)
+__global__ void __launch_bounds__(so::NUM_THREADS, CTAS)
     k_shared_out(const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_uv,
                  const __grid_constant__ CUtensorMap tm_lo, const so::Params p) {
+  constexpr int RSTEP = CTAS == 1 ? 8 : 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -646,7 +647,6 @@ __global__ void __launch_bounds__(so::NUM_THREADS, 2)
     const int row0 = 16 * (warp - 4);
     const int64_t pr0 = (static_cast<int64_t>(unit) + k0) * p.part_rows + blk % p.group * QROWS + row0;
     using so::MAX_PARTS;
-    constexpr int RSTEP = 4;
     float w[MAX_PARTS] = {0.f, 0.f, 0.f}, ws = 0.f, ls = 0.f, M = 0.f, Zp = 0.f;
     bool valid = false;
     if (lane < 16 && t0 + row0 + lane < p.T) {
@@ -671,23 +671,31 @@ __global__ void __launch_bounds__(so::NUM_THREADS, 2)
       }
     }
     const uint32_t rows_ok = __ballot_sync(0xffffffffu, valid);
-    // the prefix's share of RSTEP rows, lane l the columns 4 l .. 4 l + 3; the first ones before the product is done
+    // the prefix's share of RSTEP rows, lane l the columns 4 l .. 4 l + 3; the
+    // first ones before the product is done. All loads of a step go out together
+    // (a partial past np is read at the last one's place, with weight 0).
     float4 acc[RSTEP];
     auto load_rows = [&](int i0) {
 #pragma unroll
-      for (int i = 0; i < RSTEP; ++i) {
-        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < RSTEP; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < np; k += 2) {
+        const float *src = p.part_o + (pr0 + i0 + static_cast<int64_t>(k) * p.part_rows) * DV + 4 * lane;
+        const int64_t next = k + 1 < np ? static_cast<int64_t>(p.part_rows) * DV : 0;
+        const float wa = k == 0 ? w[0] : w[2], wb = k == 0 ? w[1] : 0.f;
+        float4 x[RSTEP], y[RSTEP];
 #pragma unroll
-        for (int k = 0; k < MAX_PARTS; ++k) {
-          const float wk = __shfl_sync(0xffffffffu, w[k], i0 + i);
-          if (k < np && (rows_ok >> (i0 + i) & 1)) {
-            const float4 x = __ldcg(
-                reinterpret_cast<const float4 *>(p.part_o + (pr0 + i0 + i + static_cast<int64_t>(k) * p.part_rows) * DV) + lane);
-            acc[i].x += x.x * wk;
-            acc[i].y += x.y * wk;
-            acc[i].z += x.z * wk;
-            acc[i].w += x.w * wk;
-          }
+        for (int i = 0; i < RSTEP; ++i) {
+          const bool ok = rows_ok >> (i0 + i) & 1;
+          x[i] = ok ? __ldcg(reinterpret_cast<const float4 *>(src + i * DV)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          y[i] = ok ? __ldcg(reinterpret_cast<const float4 *>(src + next + i * DV)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < RSTEP; ++i) {
+          const float w0 = __shfl_sync(0xffffffffu, wa, i0 + i), w1 = __shfl_sync(0xffffffffu, wb, i0 + i);
+          acc[i].x += x[i].x * w0 + y[i].x * w1;
+          acc[i].y += x[i].y * w0 + y[i].y * w1;
+          acc[i].z += x[i].z * w0 + y[i].z * w1;
+          acc[i].w += x[i].w * w0 + y[i].w * w1;
         }
       }
     };

@@ -296,21 +296,23 @@ __global__ void __launch_bounds__(256) k_simt_expand(CacheView cache, int seq, i
 // Shared-prefix decode, one block per (token row t, head h): one online
 // softmax over the P expanded prefix keys (score qa . [kc ; kr], value v) and
 // the row's visible suffix positions P .. (score q_lat . c_KV + q_R . k_R,
-// value c_KV, taken through W_UV at the end). Keys go in chunks of 256: eight
-// lanes form a score, then the threads, as `slices` groups of `width` output
-// columns, add the chunk's weighted values. fp32 throughout; q_lat [T][n_h][d_c]
-// fp32. Dynamic shared memory: (d_h + d_r) + 2 d_c floats.
+// value c_KV, taken through W_UV at the end). Keys go in chunks of 1024: eight
+// lanes form a score, then the threads, as groups of 2^k >= columns, add the
+// chunk's weighted values. fp32 throughout, q_lat = W_UK_h^T q_C among it.
+// Small layers have few (t, h) pairs, so a block is as wide as a block can be:
+// its time is a few dependent passes over the chunk. Dynamic shared memory:
+// (d_h + d_r) + 2 d_c floats.
 template <typename T>
-__global__ void __launch_bounds__(256) k_simt_shared(const T *__restrict__ qa, const float *__restrict__ q_lat,
-                                                     const T *__restrict__ kc, const T *__restrict__ v,
-                                                     const T *__restrict__ kr, int P, CacheView cache,
-                                                     const int32_t *__restrict__ seq_lens, int n_q, int n_h, int d_h,
-                                                     int d_c, int d_r, float scale, const T *__restrict__ W_UV,
-                                                     T *__restrict__ o, float *__restrict__ lse) {
-  constexpr int NT = 256, MAXC = 4;  // d_c <= 1024, d_h <= 256
+__global__ void __launch_bounds__(1024) k_simt_shared(const T *__restrict__ qa, const T *__restrict__ W_UK,
+                                                      const T *__restrict__ kc, const T *__restrict__ v,
+                                                      const T *__restrict__ kr, int P, CacheView cache,
+                                                      const int32_t *__restrict__ seq_lens, int n_q, int n_h, int d_h,
+                                                      int d_c, int d_r, float scale, const T *__restrict__ W_UV,
+                                                      T *__restrict__ o, float *__restrict__ lse) {
+  constexpr int NT = 1024, NW = NT / 32;  // d_c <= 1024, d_h <= 256
   extern __shared__ float sh[];
   float *q_s = sh, *ql_s = sh + d_h + d_r, *oc_s = ql_s + d_c;
-  __shared__ float p_s[NT], r_s[NT / 32], x_s[NT];
+  __shared__ float p_s[NT], x_s[NT], r_s[NW];
   __shared__ int64_t row_s[NT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t = blockIdx.x / n_h, h = blockIdx.x % n_h, b = t / n_q, j = t % n_q, D = d_c + d_r;
@@ -322,29 +324,47 @@ __global__ void __launch_bounds__(256) k_simt_shared(const T *__restrict__ qa, c
   }
   const int total = L - n_q + 1 + j;  // visible positions, the prefix's P first
   const int64_t th = static_cast<int64_t>(t) * n_h + h;
-  for (int e = tid; e < d_h + d_r; e += NT) q_s[e] = ld_f(qa + th * (d_h + d_r) + e);
-  for (int e = tid; e < d_c; e += NT) ql_s[e] = q_lat[th * d_c + e];
-  const T *data = static_cast<const T *>(cache.data);
   auto pow2 = [](int n) {
     int w = 32;
-    while (w < n && w < NT) w <<= 1;
+    while (w < n) w <<= 1;
     return w;
   };
   const int wv = pow2(d_h), wc = pow2(d_c);
-  float m = -INFINITY, l = 0.f, av = 0.f, ac[MAXC] = {0.f, 0.f, 0.f, 0.f};
+  // sum of x over the threads with the same column tid % w, to the first w threads
+  auto slices = [&](float x, int w) {
+    __syncthreads();
+    x_s[tid] = x;
+    __syncthreads();
+    float s = 0.f;
+    if (tid < w)
+      for (int k = tid; k < NT; k += w) s += x_s[k];
+    return s;
+  };
+  for (int e = tid; e < d_h + d_r; e += NT) q_s[e] = ld_f(qa + th * (d_h + d_r) + e);
+  __syncthreads();
+  {  // q_lat[e] = sum_i W_UK[h d_h + i][e] q_C[i]: neighbouring threads read neighbouring columns
+    float s = 0.f;
+    const int e = tid % wc;
+    if (e < d_c)
+      for (int i = tid / wc; i < d_h; i += NT / wc) s += ld_f(W_UK + (static_cast<int64_t>(h) * d_h + i) * d_c + e) * q_s[i];
+    s = slices(s, wc);
+    if (tid < d_c) ql_s[tid] = s;
+  }
+  const T *data = static_cast<const T *>(cache.data);
+  float m = -INFINITY, l = 0.f, av = 0.f, ac = 0.f;
   for (int k0 = 0; k0 < total;) {
     const bool pre = k0 < P;
     const int n = min(NT, (pre ? P : total) - k0);
-    __syncthreads();  // q staged, and the last chunk's scores and rows no longer read
+    __syncthreads();  // queries staged, and the last chunk's weights and rows no longer read
     if (!pre && tid < n) {
       const int64_t row = cache_row(cache, b, k0 + tid);
       if (row < 0) dev_error(MLA_DEVERR_DATA);  // reads as a row of zeros
       row_s[tid] = row;
     }
     __syncthreads();
-    const int sub = tid >> 3, l8 = tid & 7;
+    const int l8 = tid & 7;
     float mx = -INFINITY;
-    for (int i = sub; i < (n + 3) / 4 * 4; i += NT / 8) {  // the four keys of a warp go round together
+    for (int i = tid >> 3; i < (n + 3) / 4 * 4; i += NT / 8) {  // the four keys of a warp go round together
       float s = 0.f;
       if (i < n) {
         if (pre) {
@@ -369,9 +389,10 @@ __global__ void __launch_bounds__(256) k_simt_shared(const T *__restrict__ qa, c
     for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
     if (lane == 0) r_s[warp] = mx;
     __syncthreads();
-    float mn = m;
+    float mn = r_s[lane];  // NW = 32 warps: one value per lane
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, r_s[w]);
+    for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+    mn = fmaxf(m, mn);
     const float alpha = __expf(m - mn);  // m = -inf on the first chunk: 0
     m = mn;
     float pv = 0.f;
@@ -381,54 +402,40 @@ __global__ void __launch_bounds__(256) k_simt_shared(const T *__restrict__ qa, c
     __syncthreads();
     if (lane == 0) r_s[warp] = pv;
     __syncthreads();
-    l *= alpha;
+    float ls = r_s[lane];
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) l += r_s[w];
+    for (int w = 16; w > 0; w >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, w);
+    l = l * alpha + ls;
     av *= alpha;
-#pragma unroll
-    for (int c = 0; c < MAXC; ++c) ac[c] *= alpha;
+    ac *= alpha;
     if (pre) {
       const int e = tid % wv;
       if (e < d_h)
         for (int i = tid / wv; i < n; i += NT / wv)
           av += p_s[i] * ld_f(v + (static_cast<int64_t>(h) * P + k0 + i) * d_h + e);
     } else {
-      for (int i = tid / wc; i < n; i += NT / wc) {
-        if (row_s[i] < 0) continue;
-        const float pi = p_s[i];
-        const T *k = data + row_s[i] * D;
-#pragma unroll
-        for (int c = 0; c < MAXC; ++c)
-          if (tid % wc + c * wc < d_c) ac[c] += pi * ld_f(k + tid % wc + c * wc);
-      }
+      const int e = tid % wc;
+      if (e < d_c)
+        for (int i = tid / wc; i < n; i += NT / wc)
+          if (row_s[i] >= 0) ac += p_s[i] * ld_f(data + row_s[i] * D + e);
     }
     k0 += n;
   }
-  // sum the slices: the suffix's latent readout, then the prefix's values
-#pragma unroll
-  for (int c = 0; c < MAXC; ++c) {
-    __syncthreads();
-    x_s[tid] = ac[c];
-    __syncthreads();
-    const int e = tid + c * wc;
-    if (tid < wc && e < d_c) {
-      float s = 0.f;
-      for (int k = tid; k < NT; k += wc) s += x_s[k];
-      oc_s[e] = s;
-    }
-  }
+  // the suffix's latent readout, then the prefix's values, summed over the groups
+  ac = slices(ac, wc);
+  if (tid < d_c) oc_s[tid] = ac;
+  av = slices(av, wv);
   __syncthreads();
-  x_s[tid] = av;
+  if (tid < d_h) x_s[tid] = av;
   __syncthreads();
   const float inv = 1.f / l;
-  for (int k = warp; k < d_h; k += NT / 32) {
+  for (int k = warp; k < d_h; k += NW) {
     const T *w = W_UV + (static_cast<int64_t>(h) * d_h + k) * d_c;
     float s = 0.f;
     for (int e = lane; e < d_c; e += 32) s += ld_f(w + e) * oc_s[e];
-    for (int e = k + lane * wv; e < NT; e += 32 * wv) s += x_s[e];
 #pragma unroll
     for (int u = 16; u > 0; u >>= 1) s += __shfl_xor_sync(0xffffffffu, s, u);
-    if (lane == 0) o[th * d_h + k] = from_f<T>(s * inv);
+    if (lane == 0) o[th * d_h + k] = from_f<T>((s + x_s[k]) * inv);
   }
   if (lse != nullptr && tid == 0) lse[th] = m + logf(l);
 }
