@@ -1273,8 +1273,13 @@ mla_status tc_decode_shared(const mla_dims *d, const void *qa, const void *kc, c
                             const mla_cache *c, const int32_t *seq_lens, int B, int n_q, const void *W_UK,
                             const void *W_UV, void *o, float *lse, void *ws, size_t ws_bytes, cudaStream_t st) {
   namespace X = mla::pfx;
-  if (c->paged && P % 64 != 0)
-    return fail(MLA_ERR_UNSUPPORTED, "decode_shared needs prefix_len to be a multiple of 64 on a paged cache");
+  // everything the suffix decode would refuse is refused here, before the first launch
+  if (c->paged && c->block_size % mla::dec::BLK != 0)
+    return fail(MLA_ERR_UNSUPPORTED, "decode_shared needs block_size to be a multiple of %d", mla::dec::BLK);
+  if (c->paged && P % mla::dec::BLK != 0)
+    return fail(MLA_ERR_UNSUPPORTED, "decode_shared needs prefix_len to be a multiple of %d on a paged cache", mla::dec::BLK);
+  if (cache_rows_of(c) >= 0x7fff0000LL)
+    return fail(MLA_ERR_UNSUPPORTED, "cache has too many rows for 32-bit TMA coordinates");
   const SharedPlan w = shared_plan(d, B, n_q, P);
   uint8_t *w8 = static_cast<uint8_t *>(ws);
   __nv_bfloat16 *q = reinterpret_cast<__nv_bfloat16 *>(w8 + w.q), *q_lo = reinterpret_cast<__nv_bfloat16 *>(w8 + w.q_lo),
@@ -1860,6 +1865,8 @@ mla_status mla_decode_shared(const mla_dims *d, const void *qa, const void *kc, 
   if (B > c->num_seqs) return fail(MLA_ERR_INVALID_ARG, "B exceeds cache->num_seqs");
   if (static_cast<int64_t>(prefix_len) + n_q > cache_capacity(c))
     return fail(MLA_ERR_INVALID_ARG, "decode_shared: prefix_len + n_q exceeds the cache's capacity");
+  if (static_cast<int64_t>(prefix_len) + n_q > INT32_MAX)
+    return fail(MLA_ERR_UNSUPPORTED, "decode_shared: prefix_len + n_q must be below 2^31");
   if (static_cast<int64_t>(B) * n_q > mla::dec::MAX_UNITS)
     return fail(MLA_ERR_UNSUPPORTED, "decode_shared supports B*n_q <= %d", mla::dec::MAX_UNITS);
   if (d->d_h > 256) return fail(MLA_ERR_UNSUPPORTED, "decode_shared: d_h must be <= 256");
