@@ -75,10 +75,11 @@ namespace dec {
 
 constexpr int D = 576, DC = 512, DR = 64, HEADS = 128, HPC = 64;
 constexpr int TILE = 256, OWN = 128, BLK = 64;  // tokens per pair tile / per CTA / per block
-// 9 warps: producers 0-2 and 8 (producer index 3), the MMA warp 3, and the
-// softmax warps 4-7 (warp w reaches tensor-memory lanes 32 (w % 4) .. + 31)
-constexpr int NUM_PRODUCERS = 4, WARP_MMA = 3, WARP_SOFTMAX = 4, WARP_PROD3 = 8;
-constexpr int NUM_THREADS = 32 * 9;
+// 13 warps: producers 0-2 and 8 (producer index 3), the MMA warp 3, the softmax
+// warps 4-7 and the epilogue warps 9-12 (warp w reaches tensor-memory lanes
+// 32 (w % 4) .. + 31)
+constexpr int NUM_PRODUCERS = 4, WARP_MMA = 3, WARP_SOFTMAX = 4, WARP_PROD3 = 8, WARP_EPILOGUE = 9;
+constexpr int NUM_THREADS = 32 * 13;
 constexpr int NBIG = 4;              // 32 KB ring slots; big slot s belongs to producer s
 // the small slot's producer; Q's three 24 KB boxes come from producers 0-2
 // (each waits Q's empty barrier for every piece, so each wait is exact)
@@ -100,7 +101,8 @@ constexpr int BAR_Q_FULL = 0, BAR_Q_EMPTY = 1, BAR_BIG_FULL = 2, BAR_BIG_EMPTY =
               BAR_SMALL_FULL = BAR_BIG_EMPTY + NBIG,
               BAR_V_LANDED = BAR_SMALL_FULL + 1, BAR_ZERO_DONE = BAR_V_LANDED + 1, BAR_S_FULL = BAR_ZERO_DONE + 1,
               BAR_P_FULL = BAR_S_FULL + 2, BAR_O_FULL = BAR_P_FULL + 1,
-              BAR_O_FREE = BAR_O_FULL + 1, BAR_EXIT = BAR_O_FREE + 1, NUM_BARS = BAR_EXIT + 1;
+              BAR_O_FREE = BAR_O_FULL + 1, BAR_PIECE = BAR_O_FREE + 1, BAR_L_FULL = BAR_PIECE + 1,
+              BAR_L_EMPTY = BAR_L_FULL + 1, BAR_EXIT = BAR_L_EMPTY + 1, NUM_BARS = BAR_EXIT + 1;
 constexpr int MISC_RED = 256;               // float red[2][128]
 constexpr int MISC_REDL = MISC_RED + 1024;  // float redl[128]
 constexpr int MISC_INTS = MISC_REDL + 512;
@@ -141,6 +143,7 @@ struct Params {
   // [BJ + 1], then (splits > 0) piece offsets [BJ + 1]
   int32_t *plan;
   int32_t splits;   // 0: automatic plan; S > 0: every row in min(S, tiles) pieces
+  int32_t wide;     // o_lat and part_o are 32-byte aligned
   int32_t skip;     // kSkip instances: leading positions of every sequence left out (a multiple of 64 when paged)
 };
 
@@ -354,6 +357,19 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar_local, uint32_t rank)
     mbar_arrive_cluster(mapa_shared(bar_local, 0));
 }
 
+// N 32-bit words of one row, in 32-byte stores where the row allows it.
+template <int N>
+__device__ __forceinline__ void store_row(void *dst, const uint32_t (&w)[N], int wide) {
+  uint8_t *d = static_cast<uint8_t *>(dst);
+  if (wide) {
+#pragma unroll
+    for (int k = 0; k < N; k += 8) st_global_32(d + 4 * k, &w[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) *reinterpret_cast<uint4 *>(d + 4 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+  }
+}
+
 template <bool kGrouped, bool kSkip>
 __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     k_decode(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -390,6 +406,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     mbar_init(bar(BAR_P_FULL), 8);
     mbar_init(bar(BAR_O_FULL), 1);
     mbar_init(bar(BAR_O_FREE), 8);
+    mbar_init(bar(BAR_PIECE), 1);
+    mbar_init(bar(BAR_L_FULL), 4);
+    mbar_init(bar(BAR_L_EMPTY), 4);
     mbar_init(bar(BAR_EXIT), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -717,11 +736,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         if (!ok) break;
         if (!issue_pv(gi - 1, pc.t_end - 1, n == 1)) break;
+        if (elect_one()) tc_commit_pair(bar(BAR_PIECE), 0x3);
+        __syncwarp();
         ++npc;
       }
     }
   } else if (warp >= WARP_SOFTMAX && warp < WARP_SOFTMAX + 4) {
-    // ------------------------------------------------- softmax + epilogue
+    // ------------------------------------------------------------- softmax
     // A failed (timed-out) wait does not break these loops: every softmax
     // warp keeps the same sequence of named-barrier syncs and runs to the
     // end on whatever data is there; the device error word reports it.
@@ -732,7 +753,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
     const float c2 = p.scale_log2;
     PieceIter<kGrouped, kSkip> it = it0;
     Piece pc;
-    int gi = 0, gz = 0, bbase = 0;  // bbase: big-slot uses before this piece
+    int gi = 0, gz = 0, npc = 0, bbase = 0;  // bbase: big-slot uses before this piece
     while (it.next(p, pc)) {
       const int n = pc.t_end - pc.t_begin;
       float m_ref = -INFINITY, lsum = 0.f;
@@ -852,67 +873,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
           }
         }
       }
-      // ---------------------------------------------------------- epilogue
-      mbar_wait_warp(bar(BAR_O_FULL), (gi - 1) & 1, abort_flag);
-      tc_fence_after();
+      // ---- end of the piece: the row's sum to the epilogue warps (once they have
+      // read the last piece's), lse; on to the next piece while they read O out
+      if (npc > 0) mbar_wait_warp(bar(BAR_L_EMPTY), (npc - 1) & 1, abort_flag);
       redl[L] = lsum;
       named_bar_sync(1, 128);
-      const float ltot = lsum + redl[L ^ 64];
-      const float inv = 1.f / ltot;
-      const float lse_v = m_ref * p.scale + logf(ltot);
-      const int head = HPC * rank + row;
-      // A TMEM load gives each thread 32 columns of its own head, so a warp
-      // holds 32 heads x 32 columns. It transposes them, 16 columns at a time,
-      // through its threads' own 2 KB of the exchange buffer (free here: every
-      // thread has passed the last P exchange), so that a store instruction
-      // writes 8 heads x 16 contiguous columns rather than 32 heads x 4 or 8.
-      // The 16-byte chunk k of row r sits at chunk k ^ ((r >> 1) & 3) of the
-      // row's 64 bytes: both the row writes and the column reads are free of
-      // bank conflicts.
-      float *stg = reinterpret_cast<float *>(smem + OFF_XBUF + 2048 * sp);
-      const int head_w = HPC * rank + 32 * (sp & 1);  // head of the warp's row 0
-      const int sw_w = (lane >> 1) & 3;
-      const int r0 = lane >> 2, c4 = lane & 3;
-#pragma unroll 1
-      for (int q4 = 0; q4 < 8; ++q4) {
-        const int j = q4 >> 2, part = q4 & 3;
-        uint32_t o[32];
-        tmem_ld32(lane_addr + 128 * j + 32 * part, o);
-        tmem_wait_ld();
-        const int col = 256 * j + 128 * half + 32 * part;
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<float4 *>(stg + 16 * lane + 4 * (k ^ sw_w)) =
-                make_float4(__uint_as_float(o[16 * h2 + 4 * k]) * inv, __uint_as_float(o[16 * h2 + 4 * k + 1]) * inv,
-                            __uint_as_float(o[16 * h2 + 4 * k + 2]) * inv, __uint_as_float(o[16 * h2 + 4 * k + 3]) * inv);
-          __syncwarp();
-#pragma unroll
-          for (int k2 = 0; k2 < 4; ++k2) {
-            const int r = r0 + 8 * k2;
-            const float4 v = *reinterpret_cast<const float4 *>(stg + 16 * r + 4 * (c4 ^ ((r >> 1) & 3)));
-            const int64_t at = (static_cast<int64_t>(pc.single ? pc.bj : pc.slot) * HEADS + head_w + r) * DC + col +
-                               16 * h2 + 4 * c4;
-            if (pc.single)
-              *reinterpret_cast<uint2 *>(p.o_lat + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-            else
-              *reinterpret_cast<float4 *>(p.part_o + at) = v;
-          }
-          __syncwarp();  // the rows are rewritten by the next half
-        }
-      }
       if (half == 0) {
+        const float lse_v = m_ref * p.scale + logf(lsum + redl[L ^ 64]);
+        const int head = HPC * rank + row;
         if (pc.single) {
           if (p.lse != nullptr) p.lse[static_cast<int64_t>(pc.bj) * HEADS + head] = lse_v;
         } else {
           p.part_lse[static_cast<int64_t>(pc.slot) * HEADS + head] = lse_v;
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_L_FULL));
+      bbase += BIG_PER_TILE * n;
+      ++npc;
+    }
+    if (gi > 0) mbar_wait_warp(bar(BAR_O_FULL), (gi - 1) & 1, abort_flag);  // the last commit has landed
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // Warps of their own, so that a piece's O is read out while the softmax
+    // warps work on the next one (whose first PV waits for O_FREE). A thread
+    // holds 32 columns of its head at a time and stores them in whole 32-byte
+    // sectors.
+    const int sp = warp & 3, L = 32 * sp + lane, half = L >> 6;
+    const int head = HPC * static_cast<int>(rank) + (L & 63);
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
+    PieceIter<kGrouped, kSkip> it = it0;
+    Piece pc;
+    for (int npc = 0; it.next(p, pc); ++npc) {
+      mbar_wait_warp(bar(BAR_L_FULL), npc & 1, abort_flag);
+      const float inv = 1.f / (redl[L] + redl[L ^ 64]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_L_EMPTY));
+      mbar_wait_warp(bar(BAR_PIECE), npc & 1, abort_flag);
+      tc_fence_after();
+      const int64_t base =
+          (static_cast<int64_t>(pc.single ? pc.bj : pc.slot) * HEADS + head) * DC + 128 * half;
+#pragma unroll 1
+      for (int q4 = 0; q4 < 8; ++q4) {
+        uint32_t o[32];
+        tmem_ld32(lane_addr + 32 * q4, o);
+        tmem_wait_ld();
+        const int64_t at = base + 256 * (q4 >> 2) + 32 * (q4 & 3);
+        if (pc.single) {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            w[c] = pack_bf16x2(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
+          store_row<16>(p.o_lat + at, w, p.wide);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+          store_row<32>(p.part_o + at, o, p.wide);
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(bar(BAR_O_FREE), rank);
-      bbase += BIG_PER_TILE * n;
     }
   }
 

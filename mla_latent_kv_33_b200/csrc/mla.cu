@@ -1161,6 +1161,7 @@ mla_status decode_tc(const mla_dims *d, const void *q, const mla_cache *c, const
   p.plan = static_cast<int32_t *>(ws);
   p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan_bytes);
   p.part_lse = p.part_o + slots * D::HEADS * D::DC;
+  p.wide = aligned32(o_lat) && aligned32(p.part_o);
 
   p.skip = skip;
   // n_q > 1: the variant whose cluster groups follow the query positions
