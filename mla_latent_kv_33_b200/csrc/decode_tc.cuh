@@ -951,16 +951,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(2, 1, 1)
 
 // Merge the split partials of every token row that was cut by cluster range
 // boundaries: lse = log sum_s exp(lse_s), o = sum_s exp(lse_s - lse) o_s.
-// grid = BJ * 32 blocks of 128 threads: warp w of block g handles head
-// 4 (g mod 32) + w of row g / 32, lane l its float4 columns l + 32 c, c < 4.
+// grid = BJ * 16 blocks of 128 threads: warp w of block g handles heads
+// 4 (g mod 16) + w and + 64 of row g / 16, lane l the float4 columns l + 32 c,
+// c < 4. (A warp per head, twice the blocks, costs 1 us more where no row is
+// cut and 2.5 us more for 256 rows; fewer blocks leave cut rows too few warps.)
 // The partials of COMBINE_CHUNK pieces (their lse and all four float4) are
 // loaded together, one round trip per chunk, and merged with a running max.
-constexpr int COMBINE_CHUNK = 2, COMBINE_BLOCKS_PER_ROW = HEADS / 4;
+constexpr int COMBINE_CHUNK = 2, COMBINE_BLOCKS_PER_ROW = HEADS / 8;
 __global__ void __launch_bounds__(128) k_combine(Params p) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   const int bj = blockIdx.x / COMBINE_BLOCKS_PER_ROW;  // token row
-  const int head = 4 * (blockIdx.x % COMBINE_BLOCKS_PER_ROW) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int BJ = p.B * p.n_q;
   const int u = unit_of_row(p, bj);
@@ -978,65 +979,69 @@ __global__ void __launch_bounds__(128) k_combine(Params p) {
     np = p.plan[plan_pieces(BJ) + u + 1] - first;
   }
   if (np <= 1) return;
-  const float *pl = p.part_lse + static_cast<int64_t>(first) * HEADS + head;
-  const float4 *po =
-      reinterpret_cast<const float4 *>(p.part_o + (static_cast<int64_t>(first) * HEADS + head) * DC) + lane;
-  constexpr int64_t PIECE4 = static_cast<int64_t>(HEADS) * DC / 4;  // float4 stride between pieces
-  float M = -INFINITY, Z = 0.f;
-  float4 acc[4];
+#pragma unroll 1
+  for (int head = 4 * (blockIdx.x % COMBINE_BLOCKS_PER_ROW) + (threadIdx.x >> 5); head < HEADS;
+       head += 4 * COMBINE_BLOCKS_PER_ROW) {
+    const float *pl = p.part_lse + static_cast<int64_t>(first) * HEADS + head;
+    const float4 *po =
+        reinterpret_cast<const float4 *>(p.part_o + (static_cast<int64_t>(first) * HEADS + head) * DC) + lane;
+    constexpr int64_t PIECE4 = static_cast<int64_t>(HEADS) * DC / 4;  // float4 stride between pieces
+    float M = -INFINITY, Z = 0.f;
+    float4 acc[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = 0; k < np; k += COMBINE_CHUNK) {
-    float l[COMBINE_CHUNK];
-    float4 x[COMBINE_CHUNK][4];
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < np; k += COMBINE_CHUNK) {
+      float l[COMBINE_CHUNK];
+      float4 x[COMBINE_CHUNK][4];
 #pragma unroll
-    for (int u = 0; u < COMBINE_CHUNK; ++u) {
-      if (k + u < np) {
-        l[u] = __ldcg(pl + static_cast<int64_t>(k + u) * HEADS);
+      for (int u = 0; u < COMBINE_CHUNK; ++u) {
+        if (k + u < np) {
+          l[u] = __ldcg(pl + static_cast<int64_t>(k + u) * HEADS);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[u][c] = __ldcg(po + (k + u) * PIECE4 + 32 * c);
-      } else {
-        l[u] = -INFINITY;
-      }
-    }
-    float Mn = M;
-#pragma unroll
-    for (int u = 0; u < COMBINE_CHUNK; ++u) Mn = fmaxf(Mn, l[u]);
-    const float r = __expf(M - Mn);  // 0 on the first chunk (M = -inf, Mn finite)
-    Z *= r;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      acc[c].x *= r;
-      acc[c].y *= r;
-      acc[c].z *= r;
-      acc[c].w *= r;
-    }
-#pragma unroll
-    for (int u = 0; u < COMBINE_CHUNK; ++u) {
-      if (k + u < np) {
-        const float wgt = __expf(l[u] - Mn);
-        Z += wgt;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          acc[c].x += wgt * x[u][c].x;
-          acc[c].y += wgt * x[u][c].y;
-          acc[c].z += wgt * x[u][c].z;
-          acc[c].w += wgt * x[u][c].w;
+          for (int c = 0; c < 4; ++c) x[u][c] = __ldcg(po + (k + u) * PIECE4 + 32 * c);
+        } else {
+          l[u] = -INFINITY;
         }
       }
-    }
-    M = Mn;
-  }
-  const float inv = 1.f / Z;
-  uint2 *dst = reinterpret_cast<uint2 *>(p.o_lat + (static_cast<int64_t>(bj) * HEADS + head) * DC) + lane;
+      float Mn = M;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint2 out;
-    out.x = pack_bf16x2(acc[c].x * inv, acc[c].y * inv);
-    out.y = pack_bf16x2(acc[c].z * inv, acc[c].w * inv);
-    dst[32 * c] = out;
+      for (int u = 0; u < COMBINE_CHUNK; ++u) Mn = fmaxf(Mn, l[u]);
+      const float r = __expf(M - Mn);  // 0 on the first chunk (M = -inf, Mn finite)
+      Z *= r;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[c].x *= r;
+        acc[c].y *= r;
+        acc[c].z *= r;
+        acc[c].w *= r;
+      }
+#pragma unroll
+      for (int u = 0; u < COMBINE_CHUNK; ++u) {
+        if (k + u < np) {
+          const float wgt = __expf(l[u] - Mn);
+          Z += wgt;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            acc[c].x += wgt * x[u][c].x;
+            acc[c].y += wgt * x[u][c].y;
+            acc[c].z += wgt * x[u][c].z;
+            acc[c].w += wgt * x[u][c].w;
+          }
+        }
+      }
+      M = Mn;
+    }
+    const float inv = 1.f / Z;
+    uint2 *dst = reinterpret_cast<uint2 *>(p.o_lat + (static_cast<int64_t>(bj) * HEADS + head) * DC) + lane;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint2 out;
+      out.x = pack_bf16x2(acc[c].x * inv, acc[c].y * inv);
+      out.y = pack_bf16x2(acc[c].z * inv, acc[c].w * inv);
+      dst[32 * c] = out;
+    }
+    if (lane == 0 && p.lse != nullptr) p.lse[static_cast<int64_t>(bj) * HEADS + head] = M + logf(Z);
   }
-  if (lane == 0 && p.lse != nullptr) p.lse[static_cast<int64_t>(bj) * HEADS + head] = M + logf(Z);
 }
 
 }  // namespace dec
