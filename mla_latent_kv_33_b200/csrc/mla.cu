@@ -1809,7 +1809,7 @@ mla_status mla_batch_plan(const mla_cache *c, int32_t *block_table, const int32_
                                   "batch plan: set shared memory size");
   if (s != MLA_OK) return s;
   const int64_t items = std::max<int64_t>(T, static_cast<int64_t>(B) * num_shared);
-  const int64_t blocks = std::min<int64_t>((items + 2 * N::PLAN_THREADS - 1) / (2 * N::PLAN_THREADS), sm_count());
+  const int64_t blocks = std::min<int64_t>((items + N::PLAN_THREADS - 1) / N::PLAN_THREADS, sm_count());
   return launched(launch_tc(N::k_batch_plan, dim3(static_cast<unsigned>(blocks)), dim3(N::PLAN_THREADS),
                             3 * sizeof(int32_t) * B, static_cast<cudaStream_t>(stream), p),
                   "batch plan");
