@@ -201,18 +201,25 @@ __global__ void __launch_bounds__(256) k_cache_write(const V *__restrict__ rows,
     V x[U];
     int64_t dst[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u) {  // words and slots are fetched together: neither waits for the other
       const int64_t i = i0 + u * stride;
       dst[u] = -1;
       if (i < n) {
+        x[u] = rows[i];
         const int64_t t = n <= INT32_MAX ? static_cast<int32_t>(i) / vec : i / vec;
-        const int64_t slot = slots[t], c = i - t * vec;
-        if (slot >= cache_rows) {
-          if (c == 0) dev_error(MLA_DEVERR_DATA);
-        } else if (slot >= 0) {
-          x[u] = rows[i];
-          dst[u] = slot * vec + c;
-        }
+        dst[u] = slots[t];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + u * stride;
+      if (dst[u] < 0) continue;
+      const int64_t c = n <= INT32_MAX ? static_cast<int32_t>(i) % vec : i % vec;
+      if (dst[u] >= cache_rows) {
+        if (c == 0) dev_error(MLA_DEVERR_DATA);
+        dst[u] = -1;
+      } else {
+        dst[u] = dst[u] * vec + c;
       }
     }
 #pragma unroll

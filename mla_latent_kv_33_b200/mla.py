@@ -108,10 +108,10 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         if _raw_stream is not None:
-            return C.c_void_p(_raw_stream(torch.cuda.current_device()))
+            return C.c_void_p(_raw_stream(torch.cuda.current_device() if dev is None else dev))
         stream = torch.cuda.current_stream()
     return C.c_void_p(stream.cuda_stream)
 
@@ -306,7 +306,7 @@ def mla_batch_plan(cache: Cache, ctx_lens, new_lens, free_blocks, seq_lens, row_
         None if shared_blocks is None else _take(shared_blocks, i32, S, dev, "shared_blocks"), S, T,
         _take(seq_lens, i32, B, dev, "seq_lens"), _take(row_start, i32, B + 1, dev, "row_start"),
         _take(seq_idx, i32, T, dev, "seq_idx"), _take(positions, i32, T, dev, "positions"),
-        _take(slots, torch.int64, T, dev, "slots"), _take(used, i32, 1, dev, "used"), _stream(stream)), "mla_batch_plan")
+        _take(slots, torch.int64, T, dev, "slots"), _take(used, i32, 1, dev, "used"), _stream(stream, dev)), "mla_batch_plan")
 
 
 def mla_cache_write(p: Dims, rows, slots, cache: Cache, stream=None):
@@ -314,7 +314,7 @@ def mla_cache_write(p: Dims, rows, slots, cache: Cache, stream=None):
     dev, T = _call_device(stream), slots.numel()
     desc = _take_cache(p, cache, dev, "mla_cache_write")
     _check(_lib.mla_cache_write(C.byref(p), _take(rows, _storage(p), T * (p.d_c + p.d_r), dev, "rows"),
-                                _take(slots, torch.int64, T, dev, "slots"), T, desc, _stream(stream)),
+                                _take(slots, torch.int64, T, dev, "slots"), T, desc, _stream(stream, dev)),
            "mla_cache_write")
 
 
@@ -326,7 +326,7 @@ def mla_prefix_expand(p: Dims, cache: Cache, seq, W_UK, W_UV, kc, v, kr, stream=
     _check(_lib.mla_prefix_expand(C.byref(p), desc, int(seq), P, _take(W_UK, dt, HD * p.d_c, dev, "W_UK"),
                                   _take(W_UV, dt, HD * p.d_c, dev, "W_UV"), _take(kc, dt, HD * P, dev, "kc"),
                                   _take(v, dt, HD * P, dev, "v"), _take(kr, dt, P * p.d_r, dev, "kr"),
-                                  _stream(stream)), "mla_prefix_expand")
+                                  _stream(stream, dev)), "mla_prefix_expand")
 
 
 def mla_decode_shared(p: Dims, qa, kc, v, kr, cache: Cache, seq_lens, n_q, W_UK, W_UV, o, lse=None, ws=None,
@@ -347,7 +347,7 @@ def mla_decode_shared(p: Dims, qa, kc, v, kr, cache: Cache, seq_lens, n_q, W_UK,
         ws = torch.empty(workspace_size(p, OP_DECODE_SHARED, B, n_q, P), dtype=torch.uint8, device=qa.device)
     nbytes = ws.numel() * ws.element_size()
     _check(_lib.mla_decode_shared(C.byref(p), *args, _take(ws, ws.dtype, ws.numel(), dev, "ws"), nbytes,
-                                  _stream(stream)), "mla_decode_shared")
+                                  _stream(stream, dev)), "mla_decode_shared")
 
 
 def mla_selftest_timeout(wait_ns: int, scratch, stream=None):
