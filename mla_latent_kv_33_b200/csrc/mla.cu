@@ -1785,6 +1785,21 @@ mla_status mla_batch_plan(const mla_cache *c, int32_t *block_table, const int32_
       !row_start || !seq_idx || !positions || !slots || !used)
     return fail(MLA_ERR_INVALID_ARG, "batch_plan: NULL tensor argument");
   if (B > N::MAX_REQUESTS) return fail(MLA_ERR_UNSUPPORTED, "batch_plan serves at most %d requests", N::MAX_REQUESTS);
+  // blocks read the requests while others already write: no output may lie over an input
+  {
+    const auto over = [](const void *a, size_t na, const void *b, size_t nb) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+      return b != nullptr && x < y + nb && y < x + na;
+    };
+    const size_t w = sizeof(int32_t), b = B, t = T;
+    const struct { const void *p; size_t n; } outs[] = {
+        {block_table, w * b * c->max_blocks_per_seq}, {seq_lens, w * b}, {row_start, w * (b + 1)}, {seq_idx, w * t},
+        {positions, w * t}, {slots, sizeof(int64_t) * t}, {used, w}};
+    for (const auto &o : outs)
+      if (over(o.p, o.n, ctx_lens, w * b) || over(o.p, o.n, new_lens, w * b) || over(o.p, o.n, free_blocks, w * num_free) ||
+          over(o.p, o.n, shared_blocks, w * num_shared))
+        return fail(MLA_ERR_INVALID_ARG, "batch_plan: an output overlaps an input");
+  }
   N::PlanParams p{};
   p.ctx_lens = ctx_lens;
   p.new_lens = new_lens;

@@ -345,6 +345,8 @@ def mla_decode_shared(p: Dims, qa, kc, v, kr, cache: Cache, seq_lens, n_q, W_UK,
             None if lse is None else _take(lse, torch.float32, T * p.n_h, dev, "lse"))
     if ws is None:
         ws = torch.empty(workspace_size(p, OP_DECODE_SHARED, B, n_q, P), dtype=torch.uint8, device=qa.device)
+        if stream is not None:
+            ws.record_stream(stream)  # freed on return: not to be handed out before this stream is done with it
     nbytes = ws.numel() * ws.element_size()
     _check(_lib.mla_decode_shared(C.byref(p), *args, _take(ws, ws.dtype, ws.numel(), dev, "ws"), nbytes,
                                   _stream(stream, dev)), "mla_decode_shared")

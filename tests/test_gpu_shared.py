@@ -297,6 +297,54 @@ def test_two_streams_graphs_and_repeats_are_bit_equal(mla, overlap):
         mla.set_launch_overlap(was)
 
 
+def test_own_workspace_on_a_side_stream(mla):
+    """Without a workspace argument the call makes its own, which the allocator
+    must not hand out again while the side stream still uses it."""
+    import torch
+    pr = Problem(V2, "bf16", 1920, [200 + i for i in range(40)], 1, seed=14)
+    want, _, err = run_shared(mla, pr)
+    assert err == mla.MLA_OK
+    p, c, side = layer(mla, V2, "bf16"), pr.cache(mla), torch.cuda.Stream()
+    nbytes = mla.workspace_size(p, mla.OP_DECODE_SHARED, pr.B, 1, pr.P)
+    outs = [torch.zeros((pr.T, 16384), dtype=torch.bfloat16, device="cuda") for _ in range(6)]
+    torch.cuda.synchronize()
+    for o in outs:
+        mla.mla_decode_shared(p, pr.qa, pr.kc, pr.v, pr.kr, c, pr.seq_lens, 1, pr.W_UK, pr.W_UV, o, stream=side)
+        torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")  # would land in a freed workspace
+    torch.cuda.synchronize()
+    assert all(o.equal(want) for o in outs)
+
+
+def test_outputs_that_are_only_16_byte_aligned(mla):
+    import torch
+    pr = Problem(V2, "bf16", 320, [30, 700, 1], 1, seed=15)
+    p, c = layer(mla, V2, "bf16"), pr.cache(mla)
+
+    def off16(x):  # same shape, its first element 16 bytes past a 256-byte boundary
+        n = 16 // x.element_size()
+        return torch.zeros(x.numel() + n, dtype=x.dtype, device="cuda")[n:].view(x.shape)
+    kc, v, kr = off16(pr.kc), off16(pr.v), off16(pr.kr)
+    ref = [torch.zeros_like(x) for x in (pr.kc, pr.v, pr.kr)]
+    mla.mla_prefix_expand(p, c, 0, pr.W_UK, pr.W_UV, *ref)
+    mla.mla_prefix_expand(p, c, 0, pr.W_UK, pr.W_UV, kc, v, kr)
+    assert kc.equal(ref[0]) and v.equal(ref[1]) and kr.equal(ref[2])
+    want, want_lse, err = run_shared(mla, pr)
+    o = off16(want)
+    ws = torch.empty(mla.workspace_size(p, mla.OP_DECODE_SHARED, 3, 1, 320) + 16, dtype=torch.uint8, device="cuda")[16:]
+    mla.mla_decode_shared(p, off16(pr.qa).copy_(pr.qa), off16(kc).copy_(pr.kc), off16(v).copy_(pr.v),
+                          off16(kr).copy_(pr.kr), c, pr.seq_lens, 1, off16(pr.W_UK).copy_(pr.W_UK),
+                          off16(pr.W_UV).copy_(pr.W_UV), o, ws=ws)
+    assert err == mla.mla_get_device_error() == mla.MLA_OK and o.equal(want)
+    # the ordinary decode's latent readout, split rows and whole ones
+    q = torch.randn((3, 128, 576), device="cuda").to(torch.bfloat16)
+    a = torch.zeros((3, 128, 512), dtype=torch.bfloat16, device="cuda")
+    b = off16(a)
+    for splits in (0, 1, 3):
+        mla.mla_decode(p, q, c, pr.seq_lens, 1, a, num_splits=splits)
+        mla.mla_decode(p, q, c, pr.seq_lens, 1, b, num_splits=splits)
+        assert mla.mla_get_device_error() == mla.MLA_OK and a.equal(b)
+
+
 # ---------------------------------------------------------------- expansion --
 
 EXPANDS = {  # geometry, dtype, P, block size, paged

@@ -38,8 +38,8 @@ def refused(m, status, want, words):
     assert words in m._lib.mla_last_error_message().decode()
 
 
-def plan(m, c=None, table=A, ctx=A, new=A, B=8, free=A, num_free=4, shared=A, num_shared=2, T=16, seq_lens=A,
-         row_start=A, seq_idx=A, positions=A, slots=A, used=A, null_cache=False):
+def plan(m, c=None, table=1 << 24, ctx=A, new=A, B=8, free=A, num_free=4, shared=A, num_shared=2, T=16, seq_lens=2 * A,
+         row_start=2 * A, seq_idx=2 * A, positions=2 * A, slots=2 * A, used=2 * A, null_cache=False):
     c = c if c is not None else cache(m)
     return m._lib.mla_batch_plan(None if null_cache else C.byref(c), table, ctx, new, B, free, num_free, shared,
                                  num_shared, T, seq_lens, row_start, seq_idx, positions, slots, used, None)
@@ -55,6 +55,16 @@ def plan(m, c=None, table=A, ctx=A, new=A, B=8, free=A, num_free=4, shared=A, nu
 ])
 def test_batch_plan_arguments(m, kw, want, words):
     refused(m, plan(m, **kw), want, words)
+
+
+@pytest.mark.parametrize("out", ["table", "seq_lens", "row_start", "seq_idx", "positions", "slots", "used"])
+@pytest.mark.parametrize("src", ["ctx", "new", "free", "shared"])
+def test_batch_plan_outputs_may_not_overlap_inputs(m, out, src):
+    """An output that starts on an input's last element (its table of 8 x 128
+    entries starts before it and reaches into it)."""
+    last = {"ctx": 7, "new": 7, "free": 3, "shared": 1}[src]
+    x = 1 << 26
+    refused(m, plan(m, **{src: x, out: x + 4 * last if out != "table" else x - 4 * 1023}), INV, "overlaps")
 
 
 def test_batch_plan_cache(m):
