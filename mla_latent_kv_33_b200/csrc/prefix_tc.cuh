@@ -124,13 +124,12 @@ __device__ __forceinline__ void turn_rows(uint4 *stg, int lane, const uint4 (&in
 // scores of the tile two ahead are formed meanwhile. (With a buffer and an O
 // accumulator per group instead, a group waits for its own P V and the next
 // scores after every tile: 317 against 294 us for 256 rows over 16384
-// positions.) The groups share
-// one accumulator, so they share a row's reference maximum: after the maximum
-// of its tile a group takes the reference over from the other, passes it on,
-// and only then forms its exponentials. Tensor memory: three score buffers and
-// O, 128 columns each. P is written in bf16 over its scores and read as the A
-// operand of P V; V and W_UK are MN-major B operands. Rows past T and keys past
-// P load as zeros (TMA), the keys are masked.
+// positions.) The groups share one accumulator, so they share a row's reference
+// maximum: after the maximum of its tile a group takes the reference over from
+// the other, passes it on, and only then forms its exponentials. Tensor memory:
+// three score buffers and O, 128 columns each. P is written in bf16 over its
+// scores and read as the A operand of P V; V and W_UK are MN-major B operands.
+// Rows past T and keys past P load as zeros (TMA), the keys are masked.
 template <int CG>
 __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(CG, 1, 1)
     k_prefix_attend(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kc,
