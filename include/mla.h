@@ -338,7 +338,7 @@ mla_status mla_prefix_expand(const mla_dims *dims, const mla_cache *cache, int32
  * prefix's pages, a prefix token costs 82 instead of 279 Kflop per row, and 64
  * KB per batch instead of 1.1 KB per row (from L2, mostly). Measured on a B200
  * with suffixes of up to 512 tokens: equal at about 128 rows over 1024 prefix
- * tokens, 64 over 4096, 45 over 16384; 256 rows over 16384: 401 against 992 us.
+ * tokens, 64 over 4096, 45 over 16384; 256 rows over 16384: 410 against 1157 us.
  * With fewer rows mla_decode is the faster call. */
 mla_status mla_decode_shared(const mla_dims *dims, const void *qa, const void *kc, const void *v, const void *kr,
                              int32_t prefix_len, const mla_cache *cache, const int32_t *seq_lens, int32_t B,

@@ -16,7 +16,7 @@
 // 1152 bytes that one row reads; an expanded one 2 * 128 * (192 + 128) = 81,920
 // flop, and its 65,664 bytes are read once for all rows of the batch. Against
 // the ordinary decode over shared pages the call is equal at about 64 rows over
-// 4096 positions and 2.5 times as fast at 256 rows over 16384.
+// 4096 positions and 2.8 times as fast at 256 rows over 16384.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"

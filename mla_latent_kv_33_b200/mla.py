@@ -268,7 +268,11 @@ def _take(t, dtype, n, dev, what):
 
 
 def _call_device(stream):
-    return torch.cuda.current_device() if stream is None else stream.device_index
+    """The current device: a launch on a stream of another one would fail."""
+    dev = torch.cuda.current_device()
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the current device is cuda:{dev}")
+    return dev
 
 
 def _storage(p: Dims):

@@ -180,3 +180,16 @@ def test_the_binding_refuses_wrong_tensors(m, bad):
     t = Fake(**{**dict(shape=(8,)), **bad})
     with pytest.raises(ValueError, match="ctx_lens: a contiguous torch.int32 tensor of 8 elements on cuda:0"):
         m._take(t, torch.int32, 8, 0, "ctx_lens")
+
+
+@pytest.mark.parametrize("current,of_stream,ok", [(0, 0, True), (1, 1, True), (0, 1, False), (1, 0, False), (0, None, True)])
+def test_the_binding_refuses_a_stream_of_another_device(m, monkeypatch, current, of_stream, ok):
+    class Stream:
+        device_index = of_stream
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    stream = None if of_stream is None else Stream()
+    if ok:
+        assert m._call_device(stream) == current
+    else:
+        with pytest.raises(ValueError, match=f"the stream belongs to cuda:{of_stream}, the current device is cuda:{current}"):
+            m._call_device(stream)
