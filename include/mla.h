@@ -330,9 +330,9 @@ mla_status mla_prefix_expand(const mla_dims *dims, const mla_cache *cache, int32
  * The cache is read at positions prefix_len .. only; with a paged cache the
  * table entries of the prefix are not read. The tensor-core path needs
  * block_size, and with a paged cache prefix_len, to be multiples of 64; it
- * rounds W_UK_h^T q_C, the suffix's latent readout and that readout after W_UV
- * once each to the storage dtype, as mla_absorb_q, mla_decode and mla_out_proj
- * do. seq_lens[b] < prefix_len + n_q or beyond the cache capacity raises
+ * rounds W_UK_h^T q_C, the weights p and the suffix's latent readout once each to
+ * the storage dtype, as mla_absorb_q and mla_decode do; the readout after W_UV is
+ * joined with the prefix in fp32 and o rounded once. seq_lens[b] < prefix_len + n_q or beyond the cache capacity raises
  * MLA_ERR_DEVICE_DATA and leaves that sequence's outputs unwritten.
  * When it pays: against mla_decode and mla_out_proj over tables that share the
  * prefix's pages, a prefix token costs 82 instead of 279 Kflop per row, and 64

@@ -531,7 +531,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) __cluster_dims__(CG, 1, 1)
 //   o_S = W_UV_h o_lat,h  (M = 128 rows, N = 128, K = 512, fp32 in tensor memory),
 //   o = (e^lse_S o_S + sum_k e^lse_k o_k) / (e^lse_S + sum_k e^lse_k)
 // over the prefix partials o_k of the rows. o_S never leaves the SM, and is not
-// rounded on the way. Bound: the reads of o_lat, q_lo, W_UV and the partials
+// rounded on the way; o_lat was, once, to be the operand here (as between
+// mla_decode and mla_out_proj: rows that see mostly suffix end up to 0.0027 off,
+// relative, of which the output's own rounding is 0.0017. A second operand with
+// the remainder would read and write 2 x 33 MB more at 256 rows). Bound: the reads of o_lat, q_lo, W_UV and the partials
 // (128 rows over 8192 positions: 68 MB from HBM in 18 us with cold caches).
 //
 // The scores of the suffix were formed with q_lat rounded to bf16 (a
