@@ -145,10 +145,21 @@ def cache_capacity(cache: "Cache") -> int:
     return d.max_blocks_per_seq * d.block_size if d.paged else d.max_len
 
 
-def _ws(p, op, rows, n_q, ws, max_seq_len=0, num_splits=0):
+def _own_ws(nbytes, stream):
+    """Scratch that lives as long as the call. The allocator hands a block out,
+    and takes it back, in the order of the stream that is current when it is
+    allocated: made under the call's stream it can neither still be in use by
+    work queued elsewhere nor be reused before the call's kernels are done."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def _ws(p, op, rows, n_q, ws, max_seq_len=0, num_splits=0, stream=None):
     need = workspace_size(p, op, rows, n_q, max_seq_len, num_splits)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        ws = _own_ws(need, stream)
     return ws, need if ws is None else ws.numel()
 
 
@@ -158,7 +169,7 @@ def uses_tensor_cores(p: Dims, op: int) -> bool:
 
 def mla_cache_append(p: Dims, h, W_DKV, W_KR, seq_idx, positions, cache: Cache, ws=None, stream=None):
     T = h.shape[0]
-    ws, nbytes = _ws(p, OP_APPEND, T, 1, ws)
+    ws, nbytes = _ws(p, OP_APPEND, T, 1, ws, stream=stream)
     _check(_lib.mla_cache_append(C.byref(p), _ptr(h), _ptr(W_DKV), _ptr(W_KR), _ptr(seq_idx),
                                  _ptr(positions), T, C.byref(cache.desc), _ptr(ws), nbytes,
                                  _stream(stream)), "mla_cache_append")
@@ -166,7 +177,7 @@ def mla_cache_append(p: Dims, h, W_DKV, W_KR, seq_idx, positions, cache: Cache, 
 
 def mla_absorb_q(p: Dims, h, W_DQ, W_UQ, W_QR, W_UK, positions, q, ws=None, stream=None):
     T = h.shape[0]
-    ws, nbytes = _ws(p, OP_ABSORB, T, 1, ws)
+    ws, nbytes = _ws(p, OP_ABSORB, T, 1, ws, stream=stream)
     _check(_lib.mla_absorb_q(C.byref(p), _ptr(h), _ptr(W_DQ), _ptr(W_UQ), _ptr(W_QR), _ptr(W_UK),
                              _ptr(positions), T, _ptr(q), _ptr(ws), nbytes, _stream(stream)),
            "mla_absorb_q")
@@ -175,7 +186,7 @@ def mla_absorb_q(p: Dims, h, W_DQ, W_UQ, W_QR, W_UK, positions, q, ws=None, stre
 def mla_decode(p: Dims, q, cache: Cache, seq_lens, n_q, o_lat, lse=None, num_splits=0, ws=None,
                stream=None):
     B = seq_lens.shape[0]
-    ws, nbytes = _ws(p, OP_DECODE, B, n_q, ws, cache_capacity(cache), num_splits)
+    ws, nbytes = _ws(p, OP_DECODE, B, n_q, ws, cache_capacity(cache), num_splits, stream)
     _check(_lib.mla_decode(C.byref(p), _ptr(q), C.byref(cache.desc), _ptr(seq_lens), B, n_q,
                            _ptr(o_lat), _ptr(lse), num_splits, _ptr(ws), nbytes, _stream(stream)),
            "mla_decode")
@@ -191,14 +202,14 @@ def mla_decode_noalloc(p: Dims, q, cache: Cache, seq_lens, n_q, o_lat, lse=None,
 
 def mla_out_proj(p: Dims, o_lat, W_UV, o, ws=None, stream=None):
     T = o_lat.shape[0]
-    ws, nbytes = _ws(p, OP_OUT_PROJ, T, 1, ws)
+    ws, nbytes = _ws(p, OP_OUT_PROJ, T, 1, ws, stream=stream)
     _check(_lib.mla_out_proj(C.byref(p), _ptr(o_lat), _ptr(W_UV), T, _ptr(o), _ptr(ws), nbytes,
                              _stream(stream)), "mla_out_proj")
 
 
 def mla_o_proj(p: Dims, o, W_O, y, ws=None, stream=None):
     T = o.shape[0]
-    ws, nbytes = _ws(p, OP_O_PROJ, T, 1, ws)
+    ws, nbytes = _ws(p, OP_O_PROJ, T, 1, ws, stream=stream)
     _check(_lib.mla_o_proj(C.byref(p), _ptr(o), _ptr(W_O), T, _ptr(y), _ptr(ws), nbytes, _stream(stream)),
            "mla_o_proj")
 
@@ -210,7 +221,7 @@ def mla_absorb_wo(p: Dims, W_O, W_UV, W_OV, stream=None):
 
 def mla_o_proj_latent(p: Dims, o_lat, W_OV, y, ws=None, stream=None):
     T = o_lat.shape[0]
-    ws, nbytes = _ws(p, OP_O_PROJ_LATENT, T, 1, ws)
+    ws, nbytes = _ws(p, OP_O_PROJ_LATENT, T, 1, ws, stream=stream)
     _check(_lib.mla_o_proj_latent(C.byref(p), _ptr(o_lat), _ptr(W_OV), T, _ptr(y), _ptr(ws), nbytes,
                                   _stream(stream)), "mla_o_proj_latent")
 
@@ -223,7 +234,7 @@ def mla_absorb_merge(p: Dims, W_UQ, W_UK, W_UQK, stream=None):
 
 def mla_absorb_q_merged(p: Dims, h, W_DQ, W_UQK, W_QR, positions, q, ws=None, stream=None):
     T = h.shape[0]
-    ws, nbytes = _ws(p, OP_ABSORB_MERGED, T, 1, ws)
+    ws, nbytes = _ws(p, OP_ABSORB_MERGED, T, 1, ws, stream=stream)
     _check(_lib.mla_absorb_q_merged(C.byref(p), _ptr(h), _ptr(W_DQ), _ptr(W_UQK), _ptr(W_QR), _ptr(positions), T,
                                     _ptr(q), _ptr(ws), nbytes, _stream(stream)), "mla_absorb_q_merged")
 
@@ -231,7 +242,7 @@ def mla_absorb_q_merged(p: Dims, h, W_DQ, W_UQK, W_QR, positions, q, ws=None, st
 def mla_front_end(p: Dims, h, W_DKV, W_KR, W_DQ, W_UQ, W_QR, W_UK, seq_idx, positions, cache: Cache, q, ws=None,
                   stream=None):
     T = h.shape[0]
-    ws, nbytes = _ws(p, OP_FRONT_END, T, 1, ws)
+    ws, nbytes = _ws(p, OP_FRONT_END, T, 1, ws, stream=stream)
     _check(_lib.mla_front_end(C.byref(p), _ptr(h), _ptr(W_DKV), _ptr(W_KR), _ptr(W_DQ), _ptr(W_UQ), _ptr(W_QR),
                               _ptr(W_UK), _ptr(seq_idx), _ptr(positions), T, C.byref(cache.desc), _ptr(q), _ptr(ws),
                               nbytes, _stream(stream)), "mla_front_end")
@@ -245,14 +256,14 @@ def cache_rows(cache: "Cache") -> int:
 
 def mla_query_heads(p: Dims, h, W_DQ, W_UQ, W_QR, positions, qa, ws=None, stream=None):
     T = h.shape[0]
-    ws, nbytes = _ws(p, OP_QUERY_HEADS, T, 1, ws)
+    ws, nbytes = _ws(p, OP_QUERY_HEADS, T, 1, ws, stream=stream)
     _check(_lib.mla_query_heads(C.byref(p), _ptr(h), _ptr(W_DQ), _ptr(W_UQ), _ptr(W_QR), _ptr(positions), T, _ptr(qa),
                                 _ptr(ws), nbytes, _stream(stream)), "mla_query_heads")
 
 
 def mla_attend_order_a(p: Dims, qa, W_UK, W_UV, cache: Cache, seq_lens, n_q, o, ws=None, stream=None):
     B = seq_lens.shape[0]
-    ws, nbytes = _ws(p, OP_ATTEND_A, B, n_q, ws, cache_rows(cache))
+    ws, nbytes = _ws(p, OP_ATTEND_A, B, n_q, ws, cache_rows(cache), stream=stream)
     _check(_lib.mla_attend_order_a(C.byref(p), _ptr(qa), _ptr(W_UK), _ptr(W_UV), C.byref(cache.desc), _ptr(seq_lens),
                                    B, n_q, _ptr(o), _ptr(ws), nbytes, _stream(stream)), "mla_attend_order_a")
 
@@ -348,9 +359,7 @@ def mla_decode_shared(p: Dims, qa, kc, v, kr, cache: Cache, seq_lens, n_q, W_UK,
             _take(W_UV, dt, HD * p.d_c, dev, "W_UV"), _take(o, dt, T * HD, dev, "o"),
             None if lse is None else _take(lse, torch.float32, T * p.n_h, dev, "lse"))
     if ws is None:
-        ws = torch.empty(workspace_size(p, OP_DECODE_SHARED, B, n_q, P), dtype=torch.uint8, device=qa.device)
-        if stream is not None:
-            ws.record_stream(stream)  # freed on return: not to be handed out before this stream is done with it
+        ws = _own_ws(workspace_size(p, OP_DECODE_SHARED, B, n_q, P), stream)
     nbytes = ws.numel() * ws.element_size()
     _check(_lib.mla_decode_shared(C.byref(p), *args, _take(ws, ws.dtype, ws.numel(), dev, "ws"), nbytes,
                                   _stream(stream, dev)), "mla_decode_shared")
