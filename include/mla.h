@@ -100,8 +100,9 @@ typedef struct {
  * (seq_idx[t], positions[t]).
  *   h         [T][d]            W_DKV [d_c][d]     W_KR [d_r][d]
  *   seq_idx   [T] int32 device  positions [T] int32 device
- * A row whose (seq_idx, position) falls outside the cache is not written and
- * raises MLA_ERR_DEVICE_DATA in the device error word. */
+ * A row whose seq_idx is -1 is padding (mla_batch_plan's): nothing is stored for
+ * it. Any other row whose (seq_idx, position) falls outside the cache is not
+ * written and raises MLA_ERR_DEVICE_DATA in the device error word. */
 mla_status mla_cache_append(const mla_dims *dims, const void *h, const void *W_DKV,
                             const void *W_KR, const int32_t *seq_idx, const int32_t *positions,
                             int32_t T, const mla_cache *cache, void *ws, size_t ws_bytes,

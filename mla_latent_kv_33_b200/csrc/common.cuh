@@ -76,6 +76,10 @@ __device__ __forceinline__ void rope_pair(float &x0, float &x1, int pair, int d_
   rope_rotate(x0, x1, pos, rope_theta(pair, d_r, base));
 }
 
+// Sequence index of a token row that only fills a row buffer up (the batch
+// plan's padding): nothing is stored for it.
+constexpr int32_t PADDING_ROW = -1;
+
 // Physical cache row of logical (b, pos); returns -1 when out of range.
 struct CacheView {
   void *data;

@@ -828,8 +828,9 @@ __global__ void k_fin_append(const float *part, int splits, int T, int d_c, int 
   const int e = 2 * (blockIdx.x * blockDim.x + threadIdx.x);
   if (e >= D) return;
   const int64_t stride = static_cast<int64_t>(T) * D;
-  const int pos = positions[t];
-  const int64_t row = cache_row(cache, seq_idx[t], pos);
+  const int pos = positions[t], seq = seq_idx[t];
+  if (seq == PADDING_ROW) return;
+  const int64_t row = cache_row(cache, seq, pos);
   if (row < 0) {
     if (e == 0) dev_error(MLA_DEVERR_DATA);
     return;
@@ -862,8 +863,9 @@ __global__ void k_fin_front(const float *part, int splits, int T, int m_total, i
     *reinterpret_cast<uint32_t *>(cq + static_cast<int64_t>(t) * d_cq + c) = pack_bf16x2(x.x, x.y);
     return;
   }
-  const int pos = positions[t];
-  const int64_t row = cache_row(cache, seq_idx[t], pos);
+  const int pos = positions[t], seq = seq_idx[t];
+  if (seq == PADDING_ROW) return;
+  const int64_t row = cache_row(cache, seq, pos);
   if (row < 0) {
     if (e == 0) dev_error(MLA_DEVERR_DATA);
     return;

@@ -58,8 +58,9 @@ __global__ void k_simt_append_store(const float *__restrict__ rows, int D, int d
                                     double rope_base, const int32_t *__restrict__ seq_idx,
                                     const int32_t *__restrict__ positions, CacheView cache) {
   const int t = blockIdx.x;
-  const int pos = positions[t];
-  const int64_t row = cache_row(cache, seq_idx[t], pos);
+  const int pos = positions[t], seq = seq_idx[t];
+  if (seq == PADDING_ROW) return;
+  const int64_t row = cache_row(cache, seq, pos);
   if (row < 0) {
     if (threadIdx.x == 0) dev_error(MLA_DEVERR_DATA);
     return;
