@@ -279,7 +279,9 @@ mla_status mla_attend_order_a(const mla_dims *dims, const void *qa, const void *
  * rows running out) raises MLA_ERR_DEVICE_DATA: its seq_lens entry is 0, its
  * rows are padding and its table row is left as it is; the others are planned.
  * (Later requests that need a block, or a row, then run out too.) A page
- * number outside the pool raises MLA_ERR_DEVICE_DATA; rows on it get slot -1.
+ * number outside the pool, among the shared pages and the pages of this step's
+ * rows, raises MLA_ERR_DEVICE_DATA; it is entered as given, and rows on it get
+ * slot -1. (A request's other pages are not read.)
  *   cache: paged; its geometry is read (block_size, max_blocks_per_seq,
  *     num_blocks, num_seqs >= B), its data and block_table are not touched
  *   block_table [B][cache->max_blocks_per_seq], updated in place

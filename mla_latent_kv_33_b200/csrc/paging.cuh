@@ -151,7 +151,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_batch_plan(const PlanParams p)
   for (int64_t e = gtid; e < nsh; e += gstride) {
     const int b = nsh <= INT32_MAX ? static_cast<int32_t>(e) / p.num_shared : static_cast<int>(e / p.num_shared);
     const int k = static_cast<int>(e - static_cast<int64_t>(b) * p.num_shared);
-    if (ctx[b] >= 0) p.block_table[static_cast<int64_t>(b) * p.max_blocks + k] = p.shared_blocks[k];
+    if (ctx[b] < 0) continue;
+    const int32_t blk = p.shared_blocks[k];
+    if (blk < 0 || blk >= p.num_blocks) dev_error(MLA_DEVERR_DATA);  // (no new row lies on it to report it)
+    p.block_table[static_cast<int64_t>(b) * p.max_blocks + k] = blk;
   }
   // the blocks handed out: entry e of the free list goes to the request whose offset range holds e
   for (int64_t e = gtid; e < used_all; e += gstride) {
