@@ -292,8 +292,10 @@ def _storage(p: Dims):
 
 def _take_cache(p: Dims, cache: Cache, dev, what):
     data, table = cache.data, cache.block_table
-    if data.get_device() != dev or data.dtype is not _storage(p) or data.shape[-1] != p.d_c + p.d_r:
-        raise ValueError(f"{what}: a cache of {_storage(p)} rows of {p.d_c + p.d_r} on cuda:{dev} is needed, got "
+    D = p.d_c + p.d_r
+    if (data.get_device() != dev or data.dtype is not _storage(p) or data.shape[-1] != D or
+            data.numel() != data.shape[0] * data.shape[1] * D):
+        raise ValueError(f"{what}: a cache of {_storage(p)} [pages or sequences][rows][{D}] on cuda:{dev} is needed, got "
                          f"{data.dtype} {tuple(data.shape)} on {data.device}")
     if table is not None and table.get_device() != dev:
         raise ValueError(f"{what}: the block table is on {table.device}, the call on cuda:{dev}")
