@@ -274,6 +274,14 @@ mla_status mla_attend_order_a(const mla_dims *dims, const void *qa, const void *
  * are written to the first num_shared table entries of every request, whose
  * ctx_lens must count their tokens. All other table entries are left as they
  * are. Inputs are not changed, so that a step planned twice gives the same.
+ * mla_cache_append and mla_front_end skip the padding rows. The attention calls
+ * (mla_decode, mla_attend_order_a, mla_decode_shared) take the same number n_q
+ * of rows from every request, row b * n_q + j: they serve requests whose
+ * new_lens are all n_q. In a mixed step, place requests with the same number of
+ * new tokens next to each other and make one call per run of them, from request
+ * b on: q and the outputs from row row_start[b], seq_lens from entry b, a cache
+ * whose block_table starts at row b (a prompt chunk by itself: B = 1, n_q = its
+ * length). A request with no new token has no row and belongs to no run.
  * A request that cannot be planned (a negative length, a context shorter than
  * the shared pages, more tokens than a table row holds, free_blocks or the T
  * rows running out) raises MLA_ERR_DEVICE_DATA: its seq_lens entry is 0, its
@@ -332,17 +340,23 @@ mla_status mla_prefix_expand(const mla_dims *dims, const mla_cache *cache, int32
  *   o (output) [B*n_q][n_h*d_h]   lse (output, may be NULL) [B*n_q][n_h] float32
  * The cache is read at positions prefix_len .. only; with a paged cache the
  * table entries of the prefix are not read. The tensor-core path needs
- * block_size, and with a paged cache prefix_len, to be multiples of 64; it
- * rounds W_UK_h^T q_C, the weights p and the suffix's latent readout once each to
- * the storage dtype, as mla_absorb_q and mla_decode do; the readout after W_UV is
- * joined with the prefix in fp32 and o rounded once. seq_lens[b] < prefix_len + n_q or beyond the cache capacity raises
+ * block_size, and with a paged cache prefix_len, to be multiples of 64. A prefix
+ * whose last page is not full: share and expand its whole pages (prefix_len =
+ * num_shared * block_size of mla_batch_plan) and cache the tokens after them in
+ * a page of every request's own, as the beginning of its suffix.
+ * The tensor-core path rounds W_UK_h^T q_C, the weights p and the suffix's latent
+ * readout once each to the storage dtype, as mla_absorb_q and mla_decode do; the
+ * readout after W_UV is joined with the prefix in fp32 and o rounded once.
+ * seq_lens[b] < prefix_len + n_q or beyond the cache capacity raises
  * MLA_ERR_DEVICE_DATA and leaves that sequence's outputs unwritten.
  * When it pays: against mla_decode and mla_out_proj over tables that share the
  * prefix's pages, a prefix token costs 82 instead of 279 Kflop per row, and 64
  * KB per batch instead of 1.1 KB per row (from L2, mostly). Measured on a B200
- * with suffixes of up to 512 tokens: equal at about 128 rows over 1024 prefix
- * tokens, 64 over 4096, 45 over 16384; 256 rows over 16384: 410 against 1157 us.
- * With fewer rows mla_decode is the faster call. */
+ * with suffixes of up to 512 tokens: equal at 64 rows over 4096 prefix tokens and
+ * 45 over 16384; 256 rows over 16384: 402 against 1175 us (with the queries,
+ * mla_query_heads against mla_absorb_q: 524 against 1264). With fewer rows, and
+ * over 1024 tokens with any number up to 256, mla_decode is the faster call (94
+ * against 90 us at 128 rows). */
 mla_status mla_decode_shared(const mla_dims *dims, const void *qa, const void *kc, const void *v, const void *kr,
                              int32_t prefix_len, const mla_cache *cache, const int32_t *seq_lens, int32_t B,
                              int32_t n_q, const void *W_UK, const void *W_UV, void *o, float *lse, void *ws,
@@ -396,7 +410,10 @@ int32_t mla_uses_tensor_cores(const mla_dims *dims, int32_t op);
  * the cache, sequence lengths or positions, and writes any output, only
  * after that kernel has completed. The caller guarantees that the weights of
  * a call are not written by the work enqueued on the stream just before it.
- * Results are identical either way. Returns MLA_OK. No counterpart on the
+ * Results are identical either way. The second to fourth kernel of
+ * mla_decode_shared are launched like this whatever the switch says: the work
+ * ahead of them is the call's own, and W_UV is all they touch before they wait
+ * for it. Returns MLA_OK. No counterpart on the
  * pages: it is a property of how the calls are launched, not of the method. */
 mla_status mla_set_launch_overlap(int32_t enable);
 int32_t mla_get_launch_overlap(void);

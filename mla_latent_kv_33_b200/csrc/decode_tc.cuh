@@ -48,8 +48,8 @@
 //    pair (the whole warp walks the items, one elected lane issues), warps 4-7
 //    of both CTAs run the online softmax (fp32, exp2, O rescaled only when the
 //    running max grows by more than 2^8), and warps 9-12 read a piece's O out
-//    while the softmax goes on to the next piece (with the readout in the
-//    softmax warps, 256 rows of 1 to 512 tokens take 76 us, so 68.5).
+//    while the softmax goes on to the next piece (256 rows of 1 to 512 tokens:
+//    68.5 us; 76 with the readout in the softmax warps).
 //  * Work: the visible 256-token tiles of all token rows are concatenated and
 //    cut into equal contiguous ranges, one per cluster (persistent grid). A
 //    row whose tiles fall in one range is finished in place (bf16 o_lat,

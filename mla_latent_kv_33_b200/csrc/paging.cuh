@@ -63,11 +63,11 @@ __device__ __forceinline__ int last_le(const int32_t *a, int B, int32_t x) {
 }
 
 // One launch. Every block scans the requests into shared memory (row offsets
-// and free-list offsets: 12 bytes of L2 reads per request, a few hundred
-// nanoseconds for a thousand requests), then takes its stride of the requests,
+// and free-list offsets: both lengths are loaded twice, 16 bytes per request from
+// L2, a few hundred nanoseconds for a thousand requests), then takes its stride
 // of the table entries and of the rows; an entry or row finds its request by
 // bisection. Nothing is communicated between blocks, so there is no second
-// launch, no atomic and no order to depend on. Bound: latency (launch, one
+// launch, no atomic on memory and no order to depend on. Bound: latency (launch, one
 // dependent chain of loads per phase); the traffic of a step is a few hundred
 // KB at most. 64 requests with one token each take 4.3 us, 1024 requests with
 // 33 thousand rows 6.6 us (per call in a graph).

@@ -16,7 +16,8 @@
 // 1152 bytes that one row reads; an expanded one 2 * 128 * (192 + 128) = 81,920
 // flop, and its 65,664 bytes are read once for all rows of the batch. Against
 // the ordinary decode over shared pages the call is equal at about 64 rows over
-// 4096 positions and 2.8 times as fast at 256 rows over 16384.
+// 4096 positions and 2.9 times as fast at 256 rows over 16384 (402 against 1175
+// us), 2.4 times with the queries of either counted.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -110,11 +111,12 @@ __device__ __forceinline__ void turn_rows(uint4 *stg, int lane, const uint4 (&in
 // reads. Measured (256 rows over 16384 positions, the whole call): 387 us with
 // pairs, 436 with two single-CTA row groups.
 //
-// Bound: for up to 128 rows the reads of K_C and V (8192 positions: 102 us for
-// 568 MB read and 38 MB of partials written, 0.91 of the measured HBM rate; the
-// tensor pipe is 47 % active); above, the MMAs (16384 positions, 256 rows: 280
-// us, tensor pipe 70 % active at the 1.6 GHz that the power cap leaves; 1660
-// clocks per tile of a pair against 1282 of MMAs).
+// Bound: for up to 128 rows the reads of K_C and V (8192 positions: 103 us for
+// 568 MB read and 39 MB written, of which 36 are absorbed queries and their
+// remainders; 0.91 of the measured HBM rate, tensor pipe 43.5 % active); above,
+// the MMAs (16384 positions, 256 rows: 265 us, tensor pipe 70 % active at the 1.6
+// GHz that the power cap leaves; 1660 clocks per tile of a pair against 1282 of
+// MMAs).
 //
 // Roles: warps 0, 2, 3 TMA loads (K_C; V and W_UK; Q and k_R: the loads one
 // warp issues complete one after another, so they are spread over three), warp
@@ -654,8 +656,9 @@ __global__ void __launch_bounds__(so::NUM_THREADS, CTAS)
       np = k1 - k0 + 1;
     }
     // This warp joins 16 rows. Lane l < 16 weighs row l's parts while the product
-    // runs: w[k] for partial k (at most three clusters share a unit: it has at
-    // least 128 / 148 of a range's tiles), ws for the suffix, normalised.
+    // runs: w[k] for partial k (at most three clusters share a unit: there are at
+    // most 3 / 2 as many clusters as units, so that a range holds more than half a
+    // unit's tiles), ws for the suffix, normalised.
     const int row0 = 16 * (warp - 4);
     const int64_t pr0 = (static_cast<int64_t>(unit) + k0) * p.part_rows + blk % p.group * QROWS + row0;
     using so::MAX_PARTS;

@@ -142,7 +142,8 @@ __device__ __forceinline__ bool elect_one() {
 // The value lane 0 holds, known to be the same in every lane.
 __device__ __forceinline__ uint32_t warp_uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// 2^x on the special-function unit (MUFU.EX2); inputs <= 0 here.
+// 2^x on the special-function unit (MUFU.EX2). Inputs here are at most 8: scores
+// minus a reference maximum that is moved once a tile exceeds it by more than 2^8.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
